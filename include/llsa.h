@@ -385,6 +385,119 @@ llsa_status llsa_index_transpose_noalloc(const llsa_shape* shape, const int32_t*
                                          int32_t* col, llsa_stream_t stream);
 
 /*
+ * ------------------------------------------------------------------------------------------
+ * Operators beside the sparse attention (no counterpart on the pages): rotary positions for
+ * q and k, and a linear-cost sequence operator with its single-token form.  They follow the
+ * conventions at the top of this header except where stated here.
+ * ------------------------------------------------------------------------------------------
+ *
+ * Rotary positions of one or two tensors (a layer's q and k) in one launch.  Of the D channels
+ * of every row, rot channels from `first` on are turned in pairs: with n = rot / 2, pair c < n
+ * is channels (first + c, first + n + c) (the half layout) or, with LLSA_ROTARY_INTERLEAVED,
+ * (first + 2c, first + 2c + 1).  At position p, with t = p * frequencies[c] radians,
+ *   y_a = scale (x_a cos t - x_b sin t),  y_b = scale (x_b cos t + x_a sin t);
+ * the other channels are copied.  With LLSA_ROTARY_INVERSE t is negated: the gradient of the
+ * call without it (the same scale).  Angles are formed in fp64, the rotation is fp32, and the
+ * result is rounded once.
+ *
+ * x: [B, H, N, D] `dtype`, channels contiguous, with any strides of batch, head and token (in
+ * elements; x_strides NULL: contiguous), so a [B, N, H, D] projection is read in place.  x2
+ * (NULL: one tensor) has its own head count H2 and strides.  y, y2: [B, H, N, D] and
+ * [B, H2, N, D] contiguous; y may be x itself when x is contiguous (in place), otherwise no
+ * output may overlap an input or the other output (LLSA_ERR_INVALID_ARG).  These four
+ * pointers need the alignment of one element only: rows that are 16-byte aligned, with first a
+ * multiple of 8 and rot a multiple of 16, go through a kernel of 16-byte accesses.
+ * positions: int64 (int32 with LLSA_ROTARY_POSITIONS_I32) device array; token n of batch row b
+ * has position positions[b * position_stride + n] (position_stride 0: the rows share them).
+ * NULL: position n.  Any value of magnitude below 2^53 is fine.
+ * frequencies: [rot / 2] fp64 device array, radians per position.
+ * Rules: B, H, N >= 1; D == 64 or 128; rot even, 2 <= rot; first >= 0, first + rot <= D;
+ * B * max(H, H2) * N < 2^31.
+ */
+#define LLSA_ROTARY_INTERLEAVED 1
+#define LLSA_ROTARY_INVERSE 2
+#define LLSA_ROTARY_POSITIONS_I32 4
+
+typedef struct {
+  int32_t B, H, H2, N, D; /* H2: heads of x2, 0 without it */
+  int32_t dtype;          /* llsa_dtype */
+  int32_t rot, first;
+  int32_t flags;          /* LLSA_ROTARY_* bits */
+  float scale;
+} llsa_rotary_shape;
+
+llsa_status llsa_rotary(const llsa_rotary_shape* shape, const void* x, const int64_t* x_strides, const void* x2,
+                        const int64_t* x2_strides, const void* positions, int64_t position_stride,
+                        const double* frequencies, void* y, void* y2, llsa_stream_t stream);
+
+/*
+ * Linear attention with a decay for each head.  Per (batch, head), from an initial state S
+ * (D x D, rows by key channel, columns by value channel; zero without one), for t = 0, 1, ...:
+ *   S = exp(log_decay[h]) S + k_t v_t^T,   o_t = scale * S^T q_t.
+ * Cost is linear in N; there is no softmax and no normaliser.
+ *
+ * q, k, v (and dO): [B, H, N, D] `dtype`, 16-byte aligned, channels contiguous; strides of
+ * batch, head and token in elements, all three 0 for contiguous, each a positive number of
+ * whole 16 bytes (the stride of a dimension of size 1 is not looked at).  o, dq, dk, dv:
+ * [B, H, N, D] contiguous, not overlapping the inputs.
+ * log_decay: [H] fp32, natural logarithms, normally <= 0 (0: no decay; -infinity: only the
+ * token itself).  Values above 0 grow without bound and are the caller's risk.
+ * lengths: [B] int32 or NULL (every row has N tokens).  Positions at or past lengths[b] take
+ * no part whatever they hold: their o, dq, dk, dv are 0 and the final state is the state after
+ * lengths[b] tokens (0 tokens: the initial state).  A length outside [0, N] is clamped and
+ * recorded as LLSA_ERR_INTERNAL in the device status word.
+ * initial_state, final_state and their gradients: [B, H, D, D] fp32 or NULL.
+ * states: caller-owned scratch of llsa_linear_states_elems(shape) fp32 elements (NULL when that
+ * is 0) that llsa_linear_forward fills and llsa_linear_backward reads: the states at which the
+ * segments that the sequence is cut into start.
+ * Arithmetic: bf16 inputs use bf16 tensor-core products with fp32 accumulation; fp32 inputs use fp32
+ * throughout; states are fp32.  The results do not depend on timing (no atomics).
+ * Rules: B, H, N >= 1; D == 64 or 128; B * H * N < 2^31; H <= 65535.
+ */
+typedef struct {
+  int32_t B, H, N, D;
+  int32_t dtype; /* llsa_dtype */
+  float scale;   /* 1 / sqrt(D) is usual */
+  int64_t q_strides[3], k_strides[3], v_strides[3], dO_strides[3]; /* batch, head, token */
+} llsa_linear_shape;
+
+llsa_status llsa_linear_validate(const llsa_linear_shape* shape);
+size_t llsa_linear_states_elems(const llsa_linear_shape* shape);    /* fp32 elements of states */
+size_t llsa_linear_workspace_bytes(const llsa_linear_shape* shape); /* of llsa_linear_backward */
+
+llsa_status llsa_linear_forward(const llsa_linear_shape* shape, const void* q, const void* k, const void* v,
+                                const float* log_decay, const int32_t* lengths, const float* initial_state, void* o,
+                                float* final_state, float* states, llsa_stream_t stream);
+
+/*
+ * Gradients of llsa_linear_forward for dO (of o) and d_final (of final_state; NULL: 0):
+ * with G_t = dL/dS_t = exp(log_decay) G_{t+1} + scale q_t dO_t^T,
+ *   dq_t = scale S_t dO_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,  d_initial = exp(log_decay) G_0.
+ * d_initial (NULL: not wanted) is [B, H, D, D] fp32.  log_decay is a constant here.
+ * workspace: llsa_linear_workspace_bytes(shape) bytes, 16-byte aligned (NULL when that is 0).
+ */
+llsa_status llsa_linear_backward(const llsa_linear_shape* shape, const void* q, const void* k, const void* v,
+                                 const void* dO, const float* log_decay, const int32_t* lengths,
+                                 const float* initial_state, const float* d_final, const float* states, void* dq,
+                                 void* dk, void* dv, float* d_initial, void* workspace, size_t workspace_bytes,
+                                 llsa_stream_t stream);
+
+/*
+ * One token for each of B requests over a pool of states (the recurrent form):
+ *   S = exp(log_decay[h]) pool[slots[b]][h] + k v^T,  o = scale * S^T q,  pool[out_slots[b]][h] = S.
+ * q, k, v, o: [B, H, D] contiguous; the shape's N must be 1 and its strides 0 (shape->N is the
+ * tokens of one call).  pool: [pool_rows, H, D, D] fp32.  slots: [B] int32 or NULL (row b uses
+ * slot b); out_slots: [B] int32 or NULL (the state is updated in place).  Different slots
+ * keep the old state, for a token that may be rejected.  A row with a negative slot takes no
+ * part: its o is 0.  A row whose slot is not in the pool, or that would write a slot which an
+ * earlier taking-part row reads or writes or read one which such a row writes, takes no part
+ * either and is recorded as LLSA_ERR_INTERNAL.  Without slots, B <= pool_rows.
+ */
+llsa_status llsa_linear_step(const llsa_linear_shape* shape, const void* q, const void* k, const void* v,
+                             const float* log_decay, float* pool, int32_t pool_rows, const int32_t* slots,
+                             const int32_t* out_slots, void* o, llsa_stream_t stream);
+
+/*
  * Per-launch trace (instrumentation; no counterpart on the pages).  Between
  * llsa_trace_begin and llsa_trace_end, every kernel launch made by the calling host thread
  * through the calls above is bracketed by two cudaEventRecord calls on that call's stream:

@@ -62,6 +62,30 @@ class LLSAStepBuffers(ctypes.Structure):
 
 _BP = ctypes.POINTER(LLSAStepBuffers)
 
+# llsa_rotary_shape.flags
+LLSA_ROTARY_INTERLEAVED = 1
+LLSA_ROTARY_INVERSE = 2
+LLSA_ROTARY_POSITIONS_I32 = 4
+
+
+class LLSARotaryShape(ctypes.Structure):
+    """Mirror of ``llsa_rotary_shape``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "H2", "N", "D", "dtype", "rot", "first", "flags")] + \
+               [("scale", ctypes.c_float)]
+
+
+class LLSALinearShape(ctypes.Structure):
+    """Mirror of ``llsa_linear_shape``."""
+
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "N", "D", "dtype")] + [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64 * 3) for n in ("q_strides", "k_strides", "v_strides", "dO_strides")]
+
+
+_RP = ctypes.POINTER(LLSARotaryShape)
+_LP = ctypes.POINTER(LLSALinearShape)
+_I64P = ctypes.POINTER(ctypes.c_int64)
+
 SIGNATURES = {
     "llsa_status_string": (ctypes.c_char_p, [_I]),
     "llsa_validate_shape": (_I, [_SP]),
@@ -84,6 +108,13 @@ SIGNATURES = {
     "llsa_device_status": (_I, [ctypes.POINTER(ctypes.c_int32), _P]),
     "llsa_check_bounded_wait": (_I, [ctypes.c_int64, _P]),
     "llsa_gather_probe": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P]),
+    "llsa_rotary": (_I, [_RP, _P, _I64P, _P, _I64P, _P, ctypes.c_int64, _P, _P, _P, _P]),
+    "llsa_linear_validate": (_I, [_LP]),
+    "llsa_linear_states_elems": (_S, [_LP]),
+    "llsa_linear_workspace_bytes": (_S, [_LP]),
+    "llsa_linear_forward": (_I, [_LP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "llsa_linear_backward": (_I, [_LP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "llsa_linear_step": (_I, [_LP, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P]),
     "llsa_trace_begin": (_I, [ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]),
     "llsa_trace_end": (_I, [ctypes.POINTER(ctypes.c_int32)]),
     "llsa_kernel_name": (ctypes.c_char_p, [ctypes.c_int32]),

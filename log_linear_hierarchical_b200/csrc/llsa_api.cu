@@ -7,9 +7,12 @@
 #include <new>
 
 #include "attn_simt.cuh"
+#include "linear_simt.cuh"
+#include "linear_step.cuh"
 #include "probe.cuh"
 #include "pyramid.cuh"
 #include "pyramid_select.cuh"
+#include "rotary.cuh"
 #include "select.cuh"
 #include "transpose.cuh"
 #include "zorder.cuh"
@@ -301,6 +304,11 @@ enum KernelId {
   kKWaitCheck,
   kKGatherProbe,
   kKPyramidSelect,
+  kKRotary,
+  kKLinearState,
+  kKLinearScan,
+  kKLinearChunk,
+  kKLinearStep,
   kKNumKernels
 };
 
@@ -310,7 +318,8 @@ const char* const kKernelNames[kKNumKernels] = {
     "attn_bwd_dq_bf16",  "coarse_grad_reduce", "attn_bwd_dkdv_bf16", "attn_fwd_f32",
     "attn_bwd_dq_f32",   "attn_bwd_dkdv_f32",  "attn_bwd_coarse_bf16", "dkdv_order_count",
     "dkdv_order_scatter", "zorder_permute",    "transpose_scan",   "bounded_wait_check",
-    "gather_probe",      "pyramid_select"};
+    "gather_probe",      "pyramid_select",     "rotary",           "linear_state",
+    "linear_scan",       "linear_chunk",       "linear_step"};
 
 struct TraceState {
   cudaEvent_t* ev = nullptr;
@@ -860,6 +869,216 @@ struct llsa_plan {
   cudaGraphExec_t exec = nullptr;
 };
 
+// ---------------------------------------------------------------------------- rotary, linear
+namespace {
+
+constexpr int kSms = 148;  // the B200's SMs: launch shapes and scratch sizes are fixed without a device
+
+size_t dtype_bytes(int dtype) { return dtype == LLSA_BF16 ? 2 : 4; }
+
+struct Extent {
+  uintptr_t lo, hi;  // [lo, hi) in bytes
+  bool overlaps(const Extent& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// The bytes that a [B, H, N, D] tensor of these strides spans (strides of size-1 dimensions
+// are ignored); false when a stride is negative.
+bool extent_of(const void* p, int B, int H, int N, int D, const long long (&st)[3], size_t e, Extent* out) {
+  const int dims[3] = {B, H, N};
+  unsigned long long last = (unsigned long long)D;
+  for (int i = 0; i < 3; ++i) {
+    if (dims[i] > 1 && st[i] < 0) return false;
+    if (dims[i] > 1) last += (unsigned long long)(dims[i] - 1) * (unsigned long long)st[i];
+  }
+  out->lo = reinterpret_cast<uintptr_t>(p);
+  out->hi = out->lo + last * e;
+  return true;
+}
+
+void strides_or_contiguous(const int64_t* given, int H, int N, int D, long long (&st)[3]) {
+  const bool none = !given || (given[0] == 0 && given[1] == 0 && given[2] == 0);
+  st[0] = none ? (long long)H * N * D : (long long)given[0];
+  st[1] = none ? (long long)N * D : (long long)given[1];
+  st[2] = none ? (long long)D : (long long)given[2];
+}
+
+bool is_contiguous(int B, int H, int N, int D, const long long (&st)[3]) {
+  return (N == 1 || st[2] == D) && (H == 1 || st[1] == (long long)N * D) && (B == 1 || st[0] == (long long)H * N * D);
+}
+
+llsa_status rotary_launch(const llsa_rotary_shape* s, const void* x, const int64_t* xs, const void* x2,
+                          const int64_t* xs2, const void* positions, int64_t position_stride,
+                          const double* frequencies, void* y, void* y2, cudaStream_t cs) {
+  if (!s || !x || !y || !frequencies || (x2 == nullptr) != (y2 == nullptr)) return LLSA_ERR_INVALID_ARG;
+  if (s->B < 1 || s->H < 1 || s->N < 1 || s->D < 1 || s->H2 < 0 || (s->H2 > 0) != (x2 != nullptr))
+    return LLSA_ERR_INVALID_ARG;
+  if (s->dtype != LLSA_BF16 && s->dtype != LLSA_F32) return LLSA_ERR_INVALID_ARG;
+  if (s->flags & ~(LLSA_ROTARY_INTERLEAVED | LLSA_ROTARY_INVERSE | LLSA_ROTARY_POSITIONS_I32))
+    return LLSA_ERR_INVALID_ARG;
+  if (s->rot < 2 || (s->rot & 1) || s->first < 0 || s->first > s->D - s->rot) return LLSA_ERR_INVALID_ARG;
+  if (position_stride < 0) return LLSA_ERR_INVALID_ARG;
+  if (s->D != 64 && s->D != 128) return LLSA_ERR_UNSUPPORTED;
+  const int Hmax = s->H > s->H2 ? s->H : s->H2;
+  if ((long long)s->B * Hmax >= (1LL << 31) || (long long)s->B * Hmax * s->N >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
+  const size_t e = dtype_bytes(s->dtype);
+  const uintptr_t pos_align = (s->flags & LLSA_ROTARY_POSITIONS_I32) ? 4 : 8;
+  if (reinterpret_cast<uintptr_t>(frequencies) % 8 || reinterpret_cast<uintptr_t>(positions) % pos_align)
+    return LLSA_ERR_INVALID_ARG;
+
+  RotaryParams P{};
+  P.tensors = x2 ? 2 : 1;
+  const void* in[2] = {x, x2};
+  void* out[2] = {y, y2};
+  const int64_t* strides[2] = {xs, xs2};
+  const int heads[2] = {s->H, s->H2};
+  Extent ein[2], eout[2];
+  bool vec = s->first % 8 == 0 && s->rot % 16 == 0;
+  for (int i = 0; i < P.tensors; ++i) {
+    long long st[3];
+    strides_or_contiguous(strides[i], heads[i], s->N, s->D, st);
+    const long long dense[3] = {(long long)heads[i] * s->N * s->D, (long long)s->N * s->D, s->D};
+    if (reinterpret_cast<uintptr_t>(in[i]) % e || reinterpret_cast<uintptr_t>(out[i]) % e) return LLSA_ERR_INVALID_ARG;
+    if (!extent_of(in[i], s->B, heads[i], s->N, s->D, st, e, &ein[i]) ||
+        !extent_of(out[i], s->B, heads[i], s->N, s->D, dense, e, &eout[i]))
+      return LLSA_ERR_INVALID_ARG;
+    const bool in_place = in[i] == out[i] && is_contiguous(s->B, heads[i], s->N, s->D, st);
+    if (!in_place && ein[i].overlaps(eout[i])) return LLSA_ERR_INVALID_ARG;
+    const int dims[3] = {s->B, heads[i], s->N};
+    for (int d = 0; d < 3; ++d) vec = vec && (dims[d] == 1 || (st[d] * (long long)e) % 16 == 0);
+    vec = vec && aligned16(in[i]) && aligned16(out[i]);
+    P.t[i] = RotaryTensor{in[i], out[i], st[0], st[1], st[2], heads[i]};
+  }
+  if (P.tensors == 2 && (eout[0].overlaps(eout[1]) || ein[0].overlaps(eout[1]) || ein[1].overlaps(eout[0])))
+    return LLSA_ERR_INVALID_ARG;
+  P.B = s->B;
+  P.N = s->N;
+  P.D = s->D;
+  P.rot = s->rot;
+  P.first = s->first;
+  P.interleaved = (s->flags & LLSA_ROTARY_INTERLEAVED) ? 1 : 0;
+  P.inverse = (s->flags & LLSA_ROTARY_INVERSE) ? 1 : 0;
+  P.pos32 = (s->flags & LLSA_ROTARY_POSITIONS_I32) ? 1 : 0;
+  P.positions = positions;
+  P.pos_stride = position_stride;
+  P.freq = frequencies;
+  P.scale = s->scale;
+  const long long units = vec ? s->D / 16 : s->rot / 2 + (s->D - s->rot);
+  const long long blocks = ((long long)s->B * s->N * units + kRotThreads - 1) / kRotThreads;
+  if (blocks >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
+  // heads of one thread: all of them (the angles are computed once) unless that leaves fewer
+  // than four CTAs for each SM; then as many CTAs along the heads as fill them
+  const long long want = (4LL * kSms + blocks - 1) / blocks;
+  const int split = (int)(want < Hmax ? want : Hmax);
+  P.heads = (Hmax + split - 1) / split;
+  const dim3 grid((unsigned)blocks, (unsigned)((Hmax + P.heads - 1) / P.heads));
+  if (grid.y > 65535) return LLSA_ERR_UNSUPPORTED;
+  auto kern = s->dtype == LLSA_BF16 ? (vec ? rotary_vec_kernel<__nv_bfloat16> : rotary_pair_kernel<__nv_bfloat16>)
+                                    : (vec ? rotary_vec_kernel<float> : rotary_pair_kernel<float>);
+  return launch(kKRotary, cs, [&] { launch_pdl(kern, grid, dim3(kRotThreads), 0, cs, P); });
+}
+
+llsa_status linear_validate(const llsa_linear_shape* s) {
+  if (!s || s->B < 1 || s->H < 1 || s->N < 1 || s->D < 1) return LLSA_ERR_INVALID_ARG;
+  if (s->dtype != LLSA_BF16 && s->dtype != LLSA_F32) return LLSA_ERR_INVALID_ARG;
+  const long long per16 = 16 / (long long)dtype_bytes(s->dtype);
+  const int dims[3] = {s->B, s->H, s->N};
+  for (const int64_t* st : {s->q_strides, s->k_strides, s->v_strides, s->dO_strides}) {
+    if (st[0] == 0 && st[1] == 0 && st[2] == 0) continue;
+    for (int d = 0; d < 3; ++d)
+      if (dims[d] > 1 && (st[d] <= 0 || st[d] % per16 != 0 || st[d] >= (1LL << 36))) return LLSA_ERR_INVALID_ARG;
+  }
+  if (s->D != 64 && s->D != 128) return LLSA_ERR_UNSUPPORTED;
+  if (s->H > 65535 || (long long)s->B * s->H >= (1LL << 31) || (long long)s->B * s->H * s->N >= (1LL << 31))
+    return LLSA_ERR_UNSUPPORTED;
+  return LLSA_OK;
+}
+
+// Segments of a sequence.  A cut costs a second read of two of the streams (the first pass),
+// so the sequence stays whole when the (batch, head) pairs alone fill half of the GPU's CTA
+// slots; otherwise there are as many segments as fill the slots, of whole 128-token chunks.
+struct LinearCut {
+  int nseg, seg;
+};
+LinearCut linear_cut(const llsa_linear_shape* s) {
+  const long long slots = kSms * (s->D == 64 ? 2 : 1), bh = (long long)s->B * s->H;
+  const long long chunks = ((long long)s->N + 127) / 128;
+  long long n = 2 * bh > slots ? 1 : slots / bh;
+  if (n > chunks) n = chunks;
+  const long long seg = (chunks + n - 1) / n;
+  n = (chunks + seg - 1) / seg;
+  return LinearCut{(int)n, (int)(seg * 128 < (1LL << 30) ? seg * 128 : (1LL << 30))};
+}
+
+size_t linear_states(const llsa_linear_shape* s) {
+  const LinearCut c = linear_cut(s);
+  return c.nseg == 1 ? 0 : (size_t)s->B * s->H * c.nseg * s->D * s->D;
+}
+
+LinearStream linear_stream(const llsa_linear_shape* s, const void* p, const int64_t (&given)[3]) {
+  long long st[3];
+  strides_or_contiguous(given, s->H, s->N, s->D, st);
+  return LinearStream{p, st[0], st[1], st[2]};
+}
+
+template <typename T, int D, bool OUT>
+llsa_status linear_simt_launch(const LinearParams& P, int bh, cudaStream_t cs) {
+  const int smem = linear_simt_smem<D>(OUT);
+  if (!allow_smem(linear_simt_kernel<T, D, OUT>, smem)) return LLSA_ERR_CUDA;
+  const long long ctas = (long long)bh * P.nseg * P.nprob;
+  if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
+  return launch(OUT ? kKLinearChunk : kKLinearState, cs, [&] {
+    launch_pdl(linear_simt_kernel<T, D, OUT>, dim3((unsigned)ctas), dim3(kLsThreads), smem, cs, P);
+  });
+}
+
+template <bool OUT>
+llsa_status linear_pass(const llsa_linear_shape* s, const LinearParams& P, cudaStream_t cs) {
+  const int bh = s->B * s->H;
+  if (s->dtype == LLSA_BF16)
+    return s->D == 64 ? linear_simt_launch<__nv_bfloat16, 64, OUT>(P, bh, cs)
+                      : linear_simt_launch<__nv_bfloat16, 128, OUT>(P, bh, cs);
+  return s->D == 64 ? linear_simt_launch<float, 64, OUT>(P, bh, cs) : linear_simt_launch<float, 128, OUT>(P, bh, cs);
+}
+
+// Segment states of the streams (y, z) of `P.p[0]` (its first pass), then the scan.
+llsa_status linear_segment_states(const llsa_linear_shape* s, const LinearParams& P, float* states, const float* init,
+                                  float* last, cudaStream_t cs) {
+  LinearParams A = P;
+  A.nprob = 1;
+  A.per_segment = 0;
+  A.p[0].init = nullptr;
+  A.p[0].transpose = 0;
+  A.p[0].out = nullptr;
+  A.p[0].state = states;
+  llsa_status st = linear_pass<false>(s, A, cs);
+  if (st != LLSA_OK) return st;
+  const int dd4 = s->D * s->D / 4;
+  const long long ctas = (long long)s->B * s->H * (dd4 / kScanThreads);
+  return launch(kKLinearScan, cs, [&] {
+    launch_pdl(linear_scan_kernel, dim3((unsigned)ctas), dim3(kScanThreads), 0, cs, reinterpret_cast<float4*>(states),
+               reinterpret_cast<const float4*>(init), reinterpret_cast<float4*>(last), P.log_decay, P.lengths, P.H,
+               P.N, P.nseg, P.seg, dd4, P.p[0].rev);
+  });
+}
+
+LinearParams linear_params(const llsa_linear_shape* s, const float* log_decay, const int32_t* lengths) {
+  const LinearCut c = linear_cut(s);
+  LinearParams P{};
+  P.nprob = 1;
+  P.H = s->H;
+  P.N = s->N;
+  P.nseg = c.nseg;
+  P.seg = c.seg;
+  P.per_segment = c.nseg > 1;
+  P.log_decay = log_decay;
+  P.lengths = lengths;
+  return P;
+}
+
+bool aligned_or_null(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
 extern "C" {
 
 const char* llsa_status_string(llsa_status s) {
@@ -1108,6 +1327,110 @@ llsa_status llsa_gather_probe(const void* src, int64_t rows, const int32_t* tile
   if (stages == 2) return run(gather_probe_kernel<2>, gather_probe_smem<2>());
   if (stages == 4) return run(gather_probe_kernel<4>, gather_probe_smem<4>());
   return run(gather_probe_kernel<8>, gather_probe_smem<8>());
+}
+
+llsa_status llsa_rotary(const llsa_rotary_shape* shape, const void* x, const int64_t* x_strides, const void* x2,
+                        const int64_t* x2_strides, const void* positions, int64_t position_stride,
+                        const double* frequencies, void* y, void* y2, llsa_stream_t stream) {
+  return rotary_launch(shape, x, x_strides, x2, x2_strides, positions, position_stride, frequencies, y, y2,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+llsa_status llsa_linear_validate(const llsa_linear_shape* shape) { return linear_validate(shape); }
+
+size_t llsa_linear_states_elems(const llsa_linear_shape* s) {
+  return linear_validate(s) == LLSA_OK ? linear_states(s) : 0;
+}
+
+size_t llsa_linear_workspace_bytes(const llsa_linear_shape* s) {
+  return linear_validate(s) == LLSA_OK ? linear_states(s) * sizeof(float) : 0;
+}
+
+llsa_status llsa_linear_forward(const llsa_linear_shape* s, const void* q, const void* k, const void* v,
+                                const float* log_decay, const int32_t* lengths, const float* initial_state, void* o,
+                                float* final_state, float* states, llsa_stream_t stream) {
+  llsa_status st = linear_validate(s);
+  if (st != LLSA_OK) return st;
+  const size_t need = linear_states(s);
+  for (const void* p : {q, k, v, (const void*)o})
+    if (!p || !aligned16(p)) return LLSA_ERR_INVALID_ARG;
+  if (!log_decay || !aligned_or_null(log_decay, 4) || !aligned_or_null(lengths, 4) || !aligned16(initial_state) ||
+      !aligned16(final_state) || !aligned16(states))
+    return LLSA_ERR_INVALID_ARG;
+  if (need && !states) return LLSA_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LinearParams P = linear_params(s, log_decay, lengths);
+  LinearProblem& Q = P.p[0];
+  Q.x = linear_stream(s, q, s->q_strides);
+  Q.y = linear_stream(s, k, s->k_strides);
+  Q.z = linear_stream(s, v, s->v_strides);
+  Q.out = o;
+  Q.f1 = Q.f2 = s->scale;
+  Q.w = 1.0f;
+  if (need) {
+    st = linear_segment_states(s, P, states, initial_state, final_state, cs);
+    if (st != LLSA_OK) return st;
+    Q.init = states;
+  } else {
+    Q.init = initial_state;
+    Q.state = final_state;
+  }
+  return linear_pass<true>(s, P, cs);
+}
+
+llsa_status llsa_linear_backward(const llsa_linear_shape* s, const void* q, const void* k, const void* v,
+                                 const void* dO, const float* log_decay, const int32_t* lengths,
+                                 const float* initial_state, const float* d_final, const float* states, void* dq,
+                                 void* dk, void* dv, float* d_initial, void* workspace, size_t workspace_bytes,
+                                 llsa_stream_t stream) {
+  llsa_status st = linear_validate(s);
+  if (st != LLSA_OK) return st;
+  const size_t need = linear_states(s);
+  for (const void* p : {q, k, v, dO, (const void*)dq, (const void*)dk, (const void*)dv})
+    if (!p || !aligned16(p)) return LLSA_ERR_INVALID_ARG;
+  if (!log_decay || !aligned_or_null(log_decay, 4) || !aligned_or_null(lengths, 4) || !aligned16(initial_state) ||
+      !aligned16(d_final) || !aligned16(d_initial) || !aligned16(states) || !aligned16(workspace))
+    return LLSA_ERR_INVALID_ARG;
+  if (need && (!states || !workspace || workspace_bytes < need * sizeof(float))) return LLSA_ERR_WORKSPACE;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const LinearStream sq = linear_stream(s, q, s->q_strides), sk = linear_stream(s, k, s->k_strides),
+                     sv = linear_stream(s, v, s->v_strides), sd = linear_stream(s, dO, s->dO_strides);
+  float* back = need ? static_cast<float*>(workspace) : nullptr;  // the segments' G
+  LinearParams P = linear_params(s, log_decay, lengths);
+  P.nprob = 3;
+  const float f = s->scale;
+  P.p[0] = LinearProblem{sk, sq, sd, dv, need ? back : d_final, need ? nullptr : d_initial, f, 1.0f, f, 1, 0};
+  P.p[1] = LinearProblem{sv, sd, sq, dk, need ? back : d_final, nullptr, f, 1.0f, f, 1, 1};
+  P.p[2] = LinearProblem{sd, sv, sk, dq, need ? states : initial_state, nullptr, f, f, 1.0f, 0, 1};
+  if (need) {
+    st = linear_segment_states(s, P, back, d_final, d_initial, cs);
+    if (st != LLSA_OK) return st;
+  }
+  return linear_pass<true>(s, P, cs);
+}
+
+llsa_status llsa_linear_step(const llsa_linear_shape* s, const void* q, const void* k, const void* v,
+                             const float* log_decay, float* pool, int32_t pool_rows, const int32_t* slots,
+                             const int32_t* out_slots, void* o, llsa_stream_t stream) {
+  const llsa_status st = linear_validate(s);
+  if (st != LLSA_OK) return st;
+  if (s->N != 1) return LLSA_ERR_INVALID_ARG;
+  for (const int64_t* g : {s->q_strides, s->k_strides, s->v_strides})
+    if (g[0] || g[1] || g[2]) return LLSA_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, (const void*)o, (const void*)pool})
+    if (!p || !aligned16(p)) return LLSA_ERR_INVALID_ARG;
+  if (!log_decay || !aligned_or_null(log_decay, 4) || !aligned_or_null(slots, 4) || !aligned_or_null(out_slots, 4))
+    return LLSA_ERR_INVALID_ARG;
+  if (pool_rows < 1 || (!slots && s->B > pool_rows)) return LLSA_ERR_INVALID_ARG;
+  const long long ctas = (long long)s->B * s->H * (s->D / 32);
+  if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
+  const StepParams P{q, k, v, o, log_decay, pool, slots, out_slots, s->B, s->H, pool_rows, s->scale};
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  auto kern = s->dtype == LLSA_BF16
+                  ? (s->D == 64 ? linear_step_kernel<__nv_bfloat16, 64> : linear_step_kernel<__nv_bfloat16, 128>)
+                  : (s->D == 64 ? linear_step_kernel<float, 64> : linear_step_kernel<float, 128>);
+  return launch(kKLinearStep, cs,
+                [&] { launch_pdl(kern, dim3((unsigned)ctas), dim3(kStepThreads), 0, cs, P); });
 }
 
 llsa_status llsa_trace_begin(void** events, int32_t* kernel_ids, int32_t capacity) {
