@@ -9,6 +9,7 @@
 #include "attn_simt.cuh"
 #include "linear_simt.cuh"
 #include "linear_step.cuh"
+#include "linear_tc.cuh"
 #include "probe.cuh"
 #include "pyramid.cuh"
 #include "pyramid_select.cuh"
@@ -1031,12 +1032,71 @@ llsa_status linear_simt_launch(const LinearParams& P, int bh, cudaStream_t cs) {
   });
 }
 
+// A token stream as [B][H][N][D] bf16 (its own strides; any for a dimension of size 1), box =
+// 64 channels x 128 tokens with 128-byte swizzle; tokens past N are read as zeros.
+bool make_stream_map(CUtensorMap* m, const LinearStream& t, int B, int H, int N, int D) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)H, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)(N > 1 ? t.sn : D) * 2, (cuuint64_t)(H > 1 ? t.sh : D) * 2,
+                           (cuuint64_t)(B > 1 ? t.sb : D) * 2};
+  cuuint32_t box[4] = {64u, (cuuint32_t)kLtChunk, 1u, 1u};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An output [B*H][N][D]: a stored box is clipped at token N of its head.
+bool make_out_map(CUtensorMap* m, void* out, int BH, int N, int D) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)kLtChunk, 1u};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool OUT>
+llsa_status linear_tc_launch(const llsa_linear_shape* s, const LinearParams& P, cudaStream_t cs) {
+  using Cfg = LtCfg<D, OUT>;
+  if (!allow_smem(linear_tc_kernel<D, OUT>, Cfg::smem)) return LLSA_ERR_CUDA;
+  LinearTcParams Q{};
+  Q.P = P;
+  int used = 0;
+  LinearStream seen[7];
+  auto stream_map = [&](const LinearStream& t) {  // one map for a tensor that several problems read
+    for (int i = 0; i < used; ++i)
+      if (seen[i].p == t.p && seen[i].sb == t.sb && seen[i].sh == t.sh && seen[i].sn == t.sn) return i;
+    if (!make_stream_map(&Q.map[used], t, s->B, s->H, s->N, D)) return -1;
+    seen[used] = t;
+    return used++;
+  };
+  for (int i = 0; i < P.nprob; ++i) {
+    Q.iy[i] = stream_map(P.p[i].y);
+    Q.iz[i] = stream_map(P.p[i].z);
+    Q.ix[i] = OUT ? stream_map(P.p[i].x) : 0;
+    if (Q.iy[i] < 0 || Q.iz[i] < 0 || Q.ix[i] < 0) return LLSA_ERR_CUDA;
+  }
+  for (int i = 0; OUT && i < P.nprob; ++i) {
+    if (!make_out_map(&Q.map[used], P.p[i].out, s->B * s->H, s->N, D)) return LLSA_ERR_CUDA;
+    Q.iout[i] = used++;
+  }
+  const long long ctas = (long long)s->B * s->H * P.nseg * P.nprob;
+  if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
+  return launch(OUT ? kKLinearChunk : kKLinearState, cs, [&] {
+    launch_pdl(linear_tc_kernel<D, OUT>, dim3((unsigned)ctas), dim3(Cfg::threads), Cfg::smem, cs, Q);
+  });
+}
+
 template <bool OUT>
 llsa_status linear_pass(const llsa_linear_shape* s, const LinearParams& P, cudaStream_t cs) {
   const int bh = s->B * s->H;
   if (s->dtype == LLSA_BF16)
-    return s->D == 64 ? linear_simt_launch<__nv_bfloat16, 64, OUT>(P, bh, cs)
-                      : linear_simt_launch<__nv_bfloat16, 128, OUT>(P, bh, cs);
+    return s->D == 64 ? linear_tc_launch<64, OUT>(s, P, cs) : linear_tc_launch<128, OUT>(s, P, cs);
   return s->D == 64 ? linear_simt_launch<float, 64, OUT>(P, bh, cs) : linear_simt_launch<float, 128, OUT>(P, bh, cs);
 }
 
