@@ -215,39 +215,37 @@ __global__ void __launch_bounds__(kLsThreads) linear_simt_kernel(const LinearPar
 // The states between segments, in place: slot s of [BH][nseg][D*D] holds segment s's own
 // state on entry and the state that the segment starts from (time order: everything before
 // it; reversed: everything after it) on return; `last` receives the state after all of them.
-// Memory latency bounds it, so a thread loads kScanAhead segments' values before it uses them.
-constexpr int kScanThreads = 128, kScanAhead = 16;
+// Memory latency bounds it: one value a thread, and kScanAhead segments' values in flight before
+// the first is used.
+constexpr int kScanThreads = 128, kScanAhead = 32;
 
 __global__ void __launch_bounds__(kScanThreads)
-    linear_scan_kernel(float4* __restrict__ states, const float4* __restrict__ init, float4* __restrict__ last,
+    linear_scan_kernel(float* __restrict__ states, const float* __restrict__ init, float* __restrict__ last,
                        const float* __restrict__ log_decay, const int* __restrict__ lengths, int H, int N, int nseg,
-                       int seg, int dd4, int rev) {
+                       int seg, int dd, int rev) {
   pdl_enter();
-  const int per = dd4 / kScanThreads;  // CTAs of one (batch, head)
+  const int per = dd / kScanThreads;  // CTAs of one (batch, head)
   const int bh = blockIdx.x / per, e = (blockIdx.x % per) * kScanThreads + threadIdx.x;
   const float a = linear_decay(log_decay, bh % H);
   const int len = linear_length(lengths, bh / H, N);
-  float4 m = init ? init[(long long)bh * dd4 + e] : make_float4(0.f, 0.f, 0.f, 0.f);
-  float4* st = states + (long long)bh * nseg * dd4 + e;
+  const float whole = expm1f(a * (float)seg);
+  float m = init ? init[(long long)bh * dd + e] : 0.0f;
+  float* st = states + (long long)bh * nseg * dd + e;
   for (int i0 = 0; i0 < nseg; i0 += kScanAhead) {
-    float4 own[kScanAhead];
+    float own[kScanAhead];
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i)
-      if (i0 + i < nseg) own[i] = st[(long long)(rev ? nseg - 1 - i0 - i : i0 + i) * dd4];
+      own[i] = i0 + i < nseg ? st[(long long)(rev ? nseg - 1 - i0 - i : i0 + i) * dd] : 0.0f;
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i)
       if (i0 + i < nseg) {
         const int s = rev ? nseg - 1 - i0 - i : i0 + i;
-        st[(long long)s * dd4] = m;
+        st[(long long)s * dd] = m;
         const int n = max(0, min(min(seg, N - s * seg), len - s * seg));
-        const float fall = expm1f(a * (float)n);
-        m.x = fmaf(m.x, fall, m.x) + own[i].x;
-        m.y = fmaf(m.y, fall, m.y) + own[i].y;
-        m.z = fmaf(m.z, fall, m.z) + own[i].z;
-        m.w = fmaf(m.w, fall, m.w) + own[i].w;
+        m = fmaf(m, n == seg ? whole : expm1f(a * (float)n), m) + own[i];
       }
   }
-  if (last) last[(long long)bh * dd4 + e] = m;
+  if (last) last[(long long)bh * dd + e] = m;
 }
 
 }  // namespace llsa

@@ -2,28 +2,30 @@
 // CTA walks the 128-token chunks of one segment (see linear_common.cuh for the operation).
 //
 // Per chunk, with the tokens' tiles X, Y, Z [128][D] brought in by TMA and the state M:
-//   1. O = X M (M as bf16 in shared memory) and S = X Y^T                      (fp32, TMEM)
-//   2. O <- f2 l^{i+1} O;  P = f1 l^{i-j} S where j <= i, else 0, as bf16 into TMEM;
-//      Y <- w l^{n-1-j} Y, as two bf16 terms (the value and its rounding's remainder; the
-//      second takes X's place)
-//   3. O += P Z,  T = Y^T Z                                                    (fp32, TMEM)
-//   4. M = l^n M + T in fp32 registers; O goes out as bf16 through X's place and a TMA store.
-// Reversed time order mirrors the weights.  The first pass over segments (OUT = false) runs only
-// the second half of 2, T and M.
+//   1. S = X Y^T and O = X M (M as bf16 in shared memory)                      (fp32, TMEM)
+//   2. Y <- w l^{n-1-j} Y, as two bf16 terms (the value and its rounding's remainder; the
+//      second takes X's place), then T = Y^T Z                                 (fp32, TMEM)
+//   3. O <- f2 l^{i+1} O;  P = f1 l^{i-j} S where j <= i, else 0, as bf16 into TMEM, then
+//      O += P Z while T is folded into M = l^n M + T (fp32 registers)
+//   4. O goes out as bf16 through X's place and a TMA store.
+// Reversed time order mirrors the weights.  The first pass over segments (OUT = false) runs
+// only 2 and M, with the next chunk's weights applied while this chunk's T is formed.
 //
 // Roundings to bf16: P and the copy of M that X multiplies, which are tensor-core operands (2^-8
 // of a term each, like the output's own rounding); the weighted Y would be a third, in the state
-// itself, which is why it is split (2^-16).
+// itself, which is why it is split (2^-16).  At D = 64 the two terms are the halves of one M = 128
+// product (M = 64 runs at half rate): lanes 0..63 hold the state's rows from the values, lanes
+// 64..127 those from the remainders, both decay alike, X meets them as one 128-row operand, and
+// they are added when the state leaves the kernel.  At D = 128 they are two products into one T.
 //
 // Weights: l^{i-j} over a 32-column block of P is (l^{i - last column}) (l^{last column - j}), two
 // factors of at most 1, so one exponential a row and block serves 32 products and nothing
 // overflows for any decay.  The 32 x 32 blocks on the diagonal take l^{i-j} from a table by
 // distance; blocks past it are stored as zeros.
 //
-// Bound: a chunk moves 4 * 128 * D * 2 bytes (2 of them read in the first pass) and the
-// tensor work is a quarter of that time, so HBM bounds it as long as the steps above overlap:
-// at D = 64 two CTAs share an SM (104 KB of shared memory, 256 TMEM columns each); at D = 128 one
-// CTA has two warpgroups that halve the columns (224 KB, 512 columns).
+// Work split: a thread has one token row (a TMEM lane) and 32 of the D columns, so 8 warps at
+// D = 64, where two CTAs share an SM (112 KB of shared memory, 256 TMEM columns each), and 16 at
+// D = 128 (one CTA, 224 KB, 512 columns): 16 warps an SM either way.
 #pragma once
 
 #include "linear_common.cuh"
@@ -31,30 +33,32 @@
 namespace llsa {
 
 constexpr int kLtChunk = 128;
+constexpr int kLtCols = 32;  // columns of a thread
 
 template <int D, bool OUT>
 struct LtCfg {
-  static constexpr int G = D / 64;                // warpgroups, and 64-channel sub-tiles of a tile
+  static constexpr int G = D / kLtCols;           // threads of a row
+  static constexpr int subs = D / 64;             // 64-channel sub-tiles of a tile
   static constexpr int compute = 128 * G;
   static constexpr int threads = compute + 64;    // + TMA warp + MMA warp
   static constexpr int ctas_per_sm = D == 64 ? 2 : 1;
   static constexpr int sub = kLtChunk * 128;      // bytes of a sub-tile
-  static constexpr int tile = G * sub;
-  // a stage is Y, Z (and X); without OUT one more tile holds Y's second term
+  static constexpr int tile = subs * sub;
+  // a stage is Y, Z (and X); without OUT two more tiles hold Y's second terms
   static constexpr int stage = (OUT ? 3 : 2) * tile;
-  static constexpr int mop = 2 * stage;           // M as bf16 (OUT), or Y's second term
-  static constexpr int tab = mop + (OUT ? D * D * 2 : tile);
+  static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's second terms
+  static constexpr int tab = mop + (OUT ? 1 : 2) * tile;
   static constexpr int bars = tab + (64 + 32) * 4;
-  static constexpr int taddr = bars + 8 * 8;
-  static constexpr int smem = 1024 + taddr + 16;
-  // TMEM columns.  D = 64: P overlays S (a warp's P block jb only covers S columns that the same
-  // warp has already read); D = 128: two warps share the lanes, so P has its own columns.
+  static constexpr int taddr = bars + 10 * 8;
+  static constexpr int smem = taddr + 16;
+  // TMEM columns.  OUT at D = 64: P overlays the S columns of blocks 0 and 1 (both are in
+  // registers before either is overwritten).  Without OUT there are two T.
   static constexpr uint32_t col_s = 0, col_o = 128, col_t = OUT ? 128 + D : 0;
   static constexpr uint32_t col_p = D == 64 ? 0 : 384;
-  static constexpr uint32_t cols = OUT ? (D == 64 ? 256 : 512) : (D == 64 ? 64 : 128);
+  static constexpr uint32_t cols = OUT ? (D == 64 ? 256 : 512) : 2 * D;
 };
 
-enum : int { kLtFull = 0, kLtS = 2, kLtP = 3, kLtO = 4, kLtM = 5, kLtOut = 6 };
+enum : int { kLtFull = 0, kLtS = 2, kLtY = 3, kLtT = 4, kLtP = 5, kLtO = 6, kLtM = 7, kLtOut = 8, kLtBars = 9 };
 
 struct alignas(64) LinearTcParams {
   CUtensorMap map[7];
@@ -101,21 +105,14 @@ __device__ __forceinline__ void lt_arrive(uint32_t bar) {
 #define LT_R8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
 #define LT_W8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
 
-// 32 columns of this warp's TMEM lanes, one lane a thread; the wait is part of it, so the
+// 16 columns of this warp's TMEM lanes, one lane a thread; the wait is part of it, so the
 // registers hold the values.
-__device__ __forceinline__ void lt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void lt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
-      : LT_R8(r, 0), LT_R8(r, 8), LT_R8(r, 16), LT_R8(r, 24)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : LT_R8(r, 0), LT_R8(r, 8)
       : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void lt_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      LT_W8(r, 0), LT_W8(r, 8), LT_W8(r, 16), LT_W8(r, 24)
       : "memory");
 }
 __device__ __forceinline__ void lt_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -127,6 +124,32 @@ __device__ __forceinline__ void lt_st16(uint32_t taddr, const uint32_t (&r)[16])
 __device__ __forceinline__ void lt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 #undef LT_R8
 #undef LT_W8
+
+// Two fp32 products, or fused multiply-adds, in one instruction.
+__device__ __forceinline__ float2 lt_mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 lt_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 lt_f2(uint32_t lo, uint32_t hi) {
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ float2 lt_bf2(uint32_t v) { return lt_f2(v << 16, v & 0xffff0000u); }
+
+// Barrier of `threads` threads (whole warps) among the CTA's, by number.
+__device__ __forceinline__ void lt_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(
@@ -147,12 +170,12 @@ template <int D, bool OUT>
 __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_per_sm)
     linear_tc_kernel(const __grid_constant__ LinearTcParams Q) {
   using Cfg = LtCfg<D, OUT>;
-  constexpr int G = Cfg::G, C = kLtChunk;
-  extern __shared__ uint8_t lt_smem[];
-  uint8_t* base = lt_smem + ((1024u - (smem_u32(lt_smem) & 1023u)) & 1023u);
+  constexpr int G = Cfg::G, C = kLtChunk, W = kLtCols;
+  extern __shared__ __align__(1024) uint8_t lt_smem[];
+  uint8_t* base = lt_smem;
   const uint32_t sb = smem_u32(base), bars = sb + Cfg::bars;
   auto bar = [&](int i) { return bars + 8u * i; };
-  float* tab = reinterpret_cast<float*>(base + Cfg::tab);  // tab[32 + n] = l^n (0 for n < 0)
+  float* tab = reinterpret_cast<float*>(base + Cfg::tab);  // tab[32 + n] = f1 l^n (0 for n < 0)
   float* colf = tab + 64;                                  // weight of a block's column j at its edge
   uint32_t* taddr = reinterpret_cast<uint32_t*>(base + Cfg::taddr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -165,13 +188,9 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   const bool rev = R.rev;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(kLtFull), 1);
-    mbar_init(bar(kLtFull + 1), 1);
-    mbar_init(bar(kLtS), 1);
-    mbar_init(bar(kLtP), Cfg::compute);
-    mbar_init(bar(kLtO), 1);
-    mbar_init(bar(kLtM), Cfg::compute);
-    mbar_init(bar(kLtOut), Cfg::compute);
+    if (sb & 1023u) record_error(LLSA_ERR_INTERNAL);  // the swizzle needs 1024-byte alignment
+    for (int i = 0; i < kLtBars; ++i)
+      mbar_init(bar(i), i == kLtY || i == kLtP || i == kLtM || i == kLtOut ? Cfg::compute : 1);
     mbar_fence_init();
   }
   if (warp == 4 * G + 1) {
@@ -184,7 +203,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   const float a = linear_decay(P.log_decay, h), a2 = a * kLog2e;
   if (threadIdx.x < 64) {
     const int n = (int)threadIdx.x - 32;
-    tab[threadIdx.x] = n < 0 ? 0.0f : exp2f(a2 * (float)n);
+    tab[threadIdx.x] = n < 0 ? 0.0f : R.f1 * exp2f(a2 * (float)n);
   } else if (threadIdx.x < 96) {
     const int j = (int)threadIdx.x - 64;
     colf[j] = exp2f(a2 * (float)(rev ? j : 31 - j));
@@ -209,7 +228,8 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       auto load = [&](int c, const CUtensorMap* m, int slot) {
         const uint32_t dst = sb + (c & 1) * Cfg::stage + slot * Cfg::tile;
 #pragma unroll
-        for (int g = 0; g < G; ++g) tma_load_4d(dst + g * Cfg::sub, m, 64 * g, chunk_at(c), h, b, bar(kLtFull + (c & 1)));
+        for (int g = 0; g < Cfg::subs; ++g)
+          tma_load_4d(dst + g * Cfg::sub, m, 64 * g, chunk_at(c), h, b, bar(kLtFull + (c & 1)));
       };
       auto load_yz = [&](int c) {
         mbar_expect_tx(bar(kLtFull + (c & 1)), (OUT ? 3 : 2) * Cfg::tile);
@@ -228,7 +248,8 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           if (!ok) break;
           const uint32_t src = sb + (c & 1) * Cfg::stage + 2 * Cfg::tile;
 #pragma unroll
-          for (int g = 0; g < G; ++g) tma_store_3d(&Q.map[Q.iout[prob]], 64 * g, chunk_at(c), bh, src + g * Cfg::sub);
+          for (int g = 0; g < Cfg::subs; ++g)
+            tma_store_3d(&Q.map[Q.iout[prob]], 64 * g, chunk_at(c), bh, src + g * Cfg::sub);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           if (c + 2 < chunks) load_yz(c + 2);
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -237,7 +258,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
             ++loaded;
           }
         } else {
-          ok = mbar_wait(bar(kLtO), c & 1);
+          ok = mbar_wait(bar(kLtT), c & 1);
           if (!ok) break;
           if (c + 2 < chunks) {
             load_yz(c + 2);
@@ -252,10 +273,13 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   } else if (warp == 4 * G + 1) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
-      constexpr uint32_t id_s = lt_idesc(128, 128, 0, 0), id_m = lt_idesc(128, D, 0, 1), id_z = lt_idesc(128, D, 0, 1),
-                         id_t = lt_idesc(D, D, 1, 1);
+      constexpr uint32_t id_s = lt_idesc(128, 128, 0, 0), id_o = lt_idesc(128, D, 0, 1), id_t = lt_idesc(128, D, 1, 1);
       constexpr uint32_t sub = Cfg::sub;
       uint32_t last = 0, last_parity = 0;
+      auto commit = [&](int which, int c) {
+        lt_commit(bar(which));
+        last = bar(which), last_parity = c & 1;
+      };
       for (int c = 0; c < chunks && ok; ++c) {
         const uint32_t st = sb + (c & 1) * Cfg::stage;
         const uint32_t y = st, z = st + Cfg::tile, x = st + 2 * Cfg::tile, m = sb + Cfg::mop;
@@ -269,207 +293,274 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
             lt_mma(tmem + Cfg::col_s, lt_desc(x + off, 16), lt_desc(y + off, 16), id_s, k > 0);
           }
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * sub + (k & 3) * 32;
-            lt_mma(tmem + Cfg::col_o, lt_desc(x + off, 16), lt_desc(m + k * 2048, D * 128), id_m, k > 0);
+          for (int k = 0; k < 8; ++k) {  // D = 64: X against the rows of both terms
+            const uint32_t off = (D == 64 ? 0 : (k >> 2) * sub) + (k & 3) * 32;
+            lt_mma(tmem + Cfg::col_o, lt_desc(x + off, 16), lt_desc(m + k * 2048, sub), id_o, k > 0);
           }
-          lt_commit(bar(kLtS));
-          last = bar(kLtS), last_parity = c & 1;
-        }
-        ok = mbar_wait(bar(kLtP), c & 1);
-        if (!ok) break;
-        lt_fence_after();
-        if (OUT) {
-#pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            lt_mma_ts(tmem + Cfg::col_o, tmem + Cfg::col_p + 8 * k, lt_desc(z + k * 2048, sub), id_z, 1);
+          commit(kLtS, c);
         }
         if (wants_state(c)) {
-          const uint32_t y2 = OUT ? x : m;
+          ok = mbar_wait(bar(kLtY), c & 1);
+          if (!ok) break;
+          lt_fence_after();
+          const uint32_t y2 = OUT ? x : m + (c & 1) * Cfg::tile;
+          const uint32_t t = tmem + Cfg::col_t + (OUT ? 0 : (c & 1) * D);
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)
-            lt_mma(tmem + Cfg::col_t, lt_desc(y + k * 2048, sub), lt_desc(z + k * 2048, sub), id_t, k > 0);
+            lt_mma(t, lt_desc(y + k * 2048, D == 64 ? y2 - y : sub), lt_desc(z + k * 2048, sub), id_t, k > 0);
+          if (D == 128) {
 #pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            lt_mma(tmem + Cfg::col_t, lt_desc(y2 + k * 2048, sub), lt_desc(z + k * 2048, sub), id_t, 1);
+            for (int k = 0; k < C / 16; ++k)
+              lt_mma(t, lt_desc(y2 + k * 2048, sub), lt_desc(z + k * 2048, sub), id_t, 1);
+          }
+          commit(kLtT, c);
         }
-        lt_commit(bar(kLtO));
-        last = bar(kLtO), last_parity = c & 1;
+        if (OUT) {
+          ok = mbar_wait(bar(kLtP), c & 1);
+          if (!ok) break;
+          lt_fence_after();
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k)
+            lt_mma_ts(tmem + Cfg::col_o, tmem + Cfg::col_p + 8 * k, lt_desc(z + k * 2048, sub), id_o, 1);
+          commit(kLtO, c);
+        }
       }
       if (!ok && last) lt_drain(last, last_parity);
     }
   } else {
     // ---------------------------------------------------------------- weights, state, output
     const int quarter = warp & 3, g = warp >> 2;
-    const int i = 32 * quarter + lane;                 // token row and TMEM lane
+    const int i = 32 * quarter + lane;                 // token row, TMEM lane, row of the state's copy
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    // state row of this thread's lane (M = 64 products use 16 lanes of each warp)
-    const int sr = D == 64 ? 16 * quarter + (lane & 15) : i;
-    const bool holds = D != 64 || lane < 16;
+    const int sr = i & (D - 1);                        // state row
+    const bool first_term = i < D;                     // at D = 64 lanes 64.. hold the second terms' rows
+    // this thread's 32 columns in a tile: four 16-byte pieces from `piece` on of sub-tile `tile_off`
+    const int tile_off = (W * g / 64) * Cfg::sub, piece = (W * g % 64) / 8;
     auto wait = [&](int which, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(which), parity)); };
-    float m[64];                                       // columns 64 g .. of state row sr
+    float2 m[W / 2];                                   // columns 32 g .. of state row sr
     {
       const float* init = R.init ? R.init + (P.per_segment ? (long long)bh * P.nseg + seg : bh) * (D * D) : nullptr;
-      if (!init) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) m[e] = 0.0f;
-      } else if (R.transpose) {
+      for (int e = 0; e < W / 2; ++e) m[e] = make_float2(0.0f, 0.0f);
+      if (init && first_term) {
+        if (R.transpose) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) m[e] = __ldg(init + (64 * g + e) * D + sr);
-      } else {
+          for (int e = 0; e < W / 2; ++e)
+            m[e] = make_float2(__ldg(init + (W * g + 2 * e) * D + sr), __ldg(init + (W * g + 2 * e + 1) * D + sr));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 64; e += 4) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(init + sr * D + 64 * g + e));
-          m[e] = v.x, m[e + 1] = v.y, m[e + 2] = v.z, m[e + 3] = v.w;
+          for (int e = 0; e < W / 4; ++e) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(init + sr * D + W * g) + e);
+            m[2 * e] = make_float2(v.x, v.y);
+            m[2 * e + 1] = make_float2(v.z, v.w);
+          }
         }
       }
     }
     auto store_m = [&]() {  // M's copy for the tensor cores
-      if (holds) {
-        uint8_t* dst = base + Cfg::mop + g * (D * 128);
+      uint8_t* dst = base + Cfg::mop + tile_off;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(dst + swz(sr, e)) =
-              make_uint4(pack_bf16(m[8 * e], m[8 * e + 1]), pack_bf16(m[8 * e + 2], m[8 * e + 3]),
-                         pack_bf16(m[8 * e + 4], m[8 * e + 5]), pack_bf16(m[8 * e + 6], m[8 * e + 7]));
-      }
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(dst + swz(i, piece + e)) =
+            make_uint4(pack_bf16(m[4 * e].x, m[4 * e].y), pack_bf16(m[4 * e + 1].x, m[4 * e + 1].y),
+                       pack_bf16(m[4 * e + 2].x, m[4 * e + 2].y), pack_bf16(m[4 * e + 3].x, m[4 * e + 3].y));
     };
-    if (OUT) {
-      store_m();
-      __syncwarp();
-      fence_proxy_async();
-      lt_arrive(bar(kLtM));
-    }
-    for (int c = 0; c < chunks && ok; ++c) {
-      const int n = min(C, hi - chunk_at(c));
-      uint8_t* st = base + (c & 1) * Cfg::stage;
-      wait(kLtFull + (c & 1), (c >> 1) & 1);  // this thread rewrites tokens that the copy brought in
-      if (OUT) wait(kLtS, c & 1);
-      if (!ok) break;
-      lt_fence_after();
-      if (OUT) {
-        const float f = R.f2 * exp2f(a2 * (float)(rev ? max(0, n - 1 - i) : i + 1));
+    // Y's rows weighted, in place and in the second terms' tile; rows behind the last token are
+    // zeroed (with Z's: their contents must not meet a product's zeros)
+    auto weight_y = [&](int c, int n) {
+      uint8_t* y = base + (c & 1) * Cfg::stage + tile_off;
+      uint8_t* y2 = OUT ? y + 2 * Cfg::tile : base + Cfg::mop + (c & 1) * Cfg::tile + tile_off;
+      if (i >= n) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 32) {
-          uint32_t r[32];
-          lt_ld32(tmem + lanes + Cfg::col_o + 64 * g + e, r);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-          lt_st32(tmem + lanes + Cfg::col_o + 64 * g + e, r);
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t at = swz(i, piece + e);
+          *reinterpret_cast<uint4*>(y + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(y2 + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(y + Cfg::tile + at) = make_uint4(0, 0, 0, 0);
         }
-#pragma unroll 1
-        for (int jb = g * (4 / G); jb < (g + 1) * (4 / G); ++jb) {
-          uint32_t p[16];
-          const int past = rev ? quarter - jb : jb - quarter;  // > 0: only masked pairs
-          if (past > 0) {
+      } else if (wants_state(c)) {
+        const float w1 = R.w * exp2f(a2 * (float)(rev ? i + 1 : n - 1 - i));
+        const float2 w = make_float2(w1, w1), minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = 0u;
-          } else {
-            uint32_t s[32];
-            lt_ld32(tmem + lanes + Cfg::col_s + 32 * jb, s);
-            float v[32];
-            if (past < 0) {
-              const float e = R.f1 * exp2f(a2 * (float)(rev ? 32 * jb - i : i - 32 * jb - 31));
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(colf + j);
-                v[j] = __uint_as_float(s[j]) * (w.x * e);
-                v[j + 1] = __uint_as_float(s[j + 1]) * (w.y * e);
-                v[j + 2] = __uint_as_float(s[j + 2]) * (w.z * e);
-                v[j + 3] = __uint_as_float(s[j + 3]) * (w.w * e);
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int dist = rev ? j - lane : lane - j;
-                const float w = tab[32 + dist] * R.f1;
-                v[j] = dist >= 0 ? __uint_as_float(s[j]) * w : 0.0f;
-              }
-            }
-            if (n < C) {  // columns behind the last token hold anything
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 32 * jb + j < n ? v[j] : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) p[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-          }
-          lt_st16(tmem + lanes + Cfg::col_p + 16 * jb, p);
-        }
-      }
-      if (wants_state(c)) {
-        const float w = R.w * exp2f(a2 * (float)(rev ? i + 1 : max(0, n - 1 - i)));
-        uint8_t* y = st + g * Cfg::sub;
-        uint8_t* y2 = (OUT ? st + 2 * Cfg::tile : base + Cfg::mop) + g * Cfg::sub;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint4* at = reinterpret_cast<uint4*>(y + swz(i, e));
-          uint4* at2 = reinterpret_cast<uint4*>(y2 + swz(i, e));
-          const uint4 v = *at;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t at = swz(i, piece + e);
+          const uint4 v = *reinterpret_cast<const uint4*>(y + at);
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t one[4], two[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float u0 = __uint_as_float(in[k] << 16) * w, u1 = __uint_as_float(in[k] & 0xffff0000u) * w;
-            one[k] = pack_bf16(u0, u1);
-            two[k] = pack_bf16(u0 - __uint_as_float(one[k] << 16), u1 - __uint_as_float(one[k] & 0xffff0000u));
+            const float2 u = lt_mul2(lt_bf2(in[k]), w);
+            one[k] = pack_bf16(u.x, u.y);
+            const float2 rest = lt_fma2(lt_bf2(one[k]), minus, u);
+            two[k] = pack_bf16(rest.x, rest.y);
           }
-          const bool in_use = i < n;
-          *at = in_use ? make_uint4(one[0], one[1], one[2], one[3]) : make_uint4(0, 0, 0, 0);
-          *at2 = in_use ? make_uint4(two[0], two[1], two[2], two[3]) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(y + at) = make_uint4(one[0], one[1], one[2], one[3]);
+          *reinterpret_cast<uint4*>(y2 + at) = make_uint4(two[0], two[1], two[2], two[3]);
         }
-      }
-      if (i >= n) {  // a row behind the last token: its Z must not meet the products' zeros
-        uint8_t* z = st + Cfg::tile + g * Cfg::sub;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(z + swz(i, e)) = make_uint4(0, 0, 0, 0);
       }
       __syncwarp();
-      if (OUT) lt_wait_st();
       fence_proxy_async();
       lt_fence_before();
-      lt_arrive(bar(kLtP));
-      wait(kLtO, c & 1);
-      if (!ok) break;
-      lt_fence_after();
-      if (wants_state(c)) {
-        // M + M (l^n - 1) rather than l^n M: a factor close to 1 repeated over thousands of
-        // chunks would add up its rounding
-        const float fall = expm1f(a * (float)n);
+      lt_arrive(bar(kLtY));
+    };
+    // M + M (l^n - 1) + T rather than l^n M + T: a factor close to 1 repeated over thousands of
+    // chunks would add up its rounding
+    auto fold_t = [&](int c, int n) {
+      const float f1 = expm1f(a * (float)n);
+      const float2 fall = make_float2(f1, f1);
 #pragma unroll
-        for (int e = 0; e < 64; e += 32) {
-          uint32_t t[32];
-          lt_ld32(tmem + lanes + Cfg::col_t + 64 * g + e, t);
+      for (int e = 0; e < W; e += 16) {
+        uint32_t t[16];
+        lt_ld16(tmem + lanes + Cfg::col_t + (OUT ? 0 : (c & 1) * D) + W * g + e, t);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m[e + j] = fmaf(m[e + j], fall, m[e + j]) + __uint_as_float(t[j]);
+        for (int j = 0; j < 8; ++j) {
+          float2& v = m[e / 2 + j];
+          const float2 d = lt_fma2(v, fall, v);
+          v = make_float2(d.x + __uint_as_float(t[2 * j]), d.y + __uint_as_float(t[2 * j + 1]));
         }
-        if (OUT && c + 1 < chunks) store_m();
-        __syncwarp();
       }
-      if (OUT) {
-        uint32_t o[32];
+    };
+    // 32 columns of P, in two halves
+    auto p_block = [&](int jb, int n, uint32_t (&p)[16]) {
+      const int past = rev ? quarter - jb : jb - quarter;  // > 0: only masked pairs
+      if (past > 0) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 32) {
-          uint32_t r[32];
-          lt_ld32(tmem + lanes + Cfg::col_o + 64 * g + e, r);
+        for (int j = 0; j < 16; ++j) p[j] = 0u;
+        return;
+      }
+      const float e1 = R.f1 * exp2f(a2 * (float)(rev ? max(0, 32 * jb - i) : max(0, i - 32 * jb - 31)));
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+      for (int q = 0; q < 32; q += 16) {
+        uint32_t s[16];
+        lt_ld16(tmem + lanes + Cfg::col_s + 32 * jb + q, s);
+        if (past < 0) {
+          const float2 e = make_float2(e1, e1);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 w = lt_mul2(*reinterpret_cast<const float2*>(colf + q + j), e);
+            const float2 v = lt_mul2(lt_f2(s[j], s[j + 1]), w);
+            s[j] = __float_as_uint(v.x);
+            s[j + 1] = __float_as_uint(v.y);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int dist = rev ? q + j - lane : lane - q - j;
+            const float w = tab[32 + dist];
+            s[j] = dist >= 0 ? __float_as_uint(__uint_as_float(s[j]) * w) : 0u;
+          }
+        }
+        if (n < C) {  // columns behind the last token hold anything
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[j] = 32 * jb + q + j < n ? s[j] : 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[q / 2 + j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+      }
+    };
+    if (OUT) {
+      store_m();
+      fence_proxy_async();
+      lt_arrive(bar(kLtM));
+      for (int c = 0; c < chunks; ++c) {
+        const int n = min(C, hi - chunk_at(c));
+        wait(kLtFull + (c & 1), (c >> 1) & 1);  // this thread rewrites tokens that the copy brought in
+        wait(kLtS, c & 1);
+        if (!ok) break;
+        lt_fence_after();
+        weight_y(c, n);
+        {
+          const float f1 = R.f2 * exp2f(a2 * (float)(rev ? max(0, n - 1 - i) : i + 1));
+          const float2 f = make_float2(f1, f1);
+#pragma unroll
+          for (int e = 0; e < W; e += 16) {
+            uint32_t r[16];
+            lt_ld16(tmem + lanes + Cfg::col_o + W * g + e, r);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float2 v = lt_mul2(lt_f2(r[j], r[j + 1]), f);
+              r[j] = __float_as_uint(v.x);
+              r[j + 1] = __float_as_uint(v.y);
+            }
+            lt_st16(tmem + lanes + Cfg::col_o + W * g + e, r);
+          }
+        }
+        uint32_t p[16];
+        p_block(g, n, p);
+        if (G == 2) lt_bar(1 + quarter, 64);  // S blocks 0 and 1 are read: P may overlay them
+        lt_st16(tmem + lanes + Cfg::col_p + 16 * g, p);
+        if (G == 2) {  // blocks 0 and 3 here, 1 and 2 there: at most two unmasked ones each
+          p_block(3 - g, n, p);
+          lt_st16(tmem + lanes + Cfg::col_p + 16 * (3 - g), p);
+        }
+        lt_wait_st();
+        lt_fence_before();
+        lt_arrive(bar(kLtP));
+        if (wants_state(c)) {
+          wait(kLtT, c & 1);
+          if (!ok) break;
+          lt_fence_after();
+          fold_t(c, n);
+          if (c + 1 < chunks) store_m();
+        }
+        wait(kLtO, c & 1);
+        if (!ok) break;
+        lt_fence_after();
+        uint32_t o[16];
+#pragma unroll
+        for (int e = 0; e < W; e += 16) {
+          uint32_t r[16];
+          lt_ld16(tmem + lanes + Cfg::col_o + W * g + e, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
             o[e / 2 + j] = i < n ? pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
         }
         fence_proxy_async();
         lt_fence_before();
         lt_arrive(bar(kLtM));
-        uint8_t* dst = st + 2 * Cfg::tile + g * Cfg::sub;
+        uint8_t* dst = base + (c & 1) * Cfg::stage + 2 * Cfg::tile + tile_off;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(dst + swz(i, e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(dst + swz(i, piece + e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         fence_proxy_async();
         lt_arrive(bar(kLtOut));
       }
+      // a warp that gave up releases the one it shares its lanes with, whose next wait gives up too
+      if (G == 2 && !ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");
+    } else {
+      for (int c = 0; c <= chunks; ++c) {
+        if (c < chunks) {
+          wait(kLtFull + (c & 1), (c >> 1) & 1);
+          if (!ok) break;
+          weight_y(c, min(C, hi - chunk_at(c)));
+        }
+        if (c > 0) {
+          wait(kLtT, (c - 1) & 1);
+          if (!ok) break;
+          lt_fence_after();
+          fold_t(c - 1, min(C, hi - chunk_at(c - 1)));
+        }
+      }
     }
-    if (ok && R.state && holds) {
-      float* dst = R.state + (OUT ? (long long)bh : (long long)bh * P.nseg + seg) * (D * D) + sr * D + 64 * g;
+    if (R.state) {
+      float* dst = R.state + (OUT ? (long long)bh : (long long)bh * P.nseg + seg) * (D * D) + sr * D + W * g;
+      if (D == 64) {  // the two terms' halves meet in the copy's place, which no product reads now
+        float2* other = reinterpret_cast<float2*>(base + Cfg::mop) + (sr * D + W * g) / 2;
+        if (!first_term) {
 #pragma unroll
-      for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(m[e], m[e + 1], m[e + 2], m[e + 3]);
+          for (int e = 0; e < W / 2; ++e) other[e] = m[e];
+        }
+        lt_bar(5, Cfg::compute);
+        if (first_term) {
+#pragma unroll
+          for (int e = 0; e < W / 2; ++e) m[e] = make_float2(m[e].x + other[e].x, m[e].y + other[e].y);
+        }
+      }
+      if (ok && first_term) {
+#pragma unroll
+        for (int e = 0; e < W / 4; ++e)
+          reinterpret_cast<float4*>(dst)[e] = make_float4(m[2 * e].x, m[2 * e].y, m[2 * e + 1].x, m[2 * e + 1].y);
+      }
     }
     if (OUT) {  // rows that take no part, behind the last chunk
       const int z0 = min(top, lo + chunks * C);

@@ -1112,12 +1112,11 @@ llsa_status linear_segment_states(const llsa_linear_shape* s, const LinearParams
   A.p[0].state = states;
   llsa_status st = linear_pass<false>(s, A, cs);
   if (st != LLSA_OK) return st;
-  const int dd4 = s->D * s->D / 4;
-  const long long ctas = (long long)s->B * s->H * (dd4 / kScanThreads);
+  const int dd = s->D * s->D;
+  const long long ctas = (long long)s->B * s->H * (dd / kScanThreads);
   return launch(kKLinearScan, cs, [&] {
-    launch_pdl(linear_scan_kernel, dim3((unsigned)ctas), dim3(kScanThreads), 0, cs, reinterpret_cast<float4*>(states),
-               reinterpret_cast<const float4*>(init), reinterpret_cast<float4*>(last), P.log_decay, P.lengths, P.H,
-               P.N, P.nseg, P.seg, dd4, P.p[0].rev);
+    launch_pdl(linear_scan_kernel, dim3((unsigned)ctas), dim3(kScanThreads), 0, cs, states, init, last, P.log_decay,
+               P.lengths, P.H, P.N, P.nseg, P.seg, dd, P.p[0].rev);
   });
 }
 
