@@ -48,7 +48,7 @@ struct LtCfg {
   static constexpr int stage = (OUT ? 3 : 2) * tile;
   static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's second terms
   static constexpr int tab = mop + (OUT ? 1 : 2) * tile;
-  static constexpr int bars = tab + (64 + 32) * 4;
+  static constexpr int bars = tab + (32 + 136 + 32 + 8) * 4;
   static constexpr int taddr = bars + 10 * 8;
   static constexpr int smem = taddr + 16;
   // TMEM columns.  OUT at D = 64: P overlays the S columns of blocks 0 and 1 (both are in
@@ -98,8 +98,10 @@ __device__ __forceinline__ void lt_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void lt_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void lt_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// One arrival for a warp, after all its lanes' writes and fences.
 __device__ __forceinline__ void lt_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  __syncwarp();
+  if (lane_id() == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 #define LT_R8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
@@ -175,8 +177,9 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   uint8_t* base = lt_smem;
   const uint32_t sb = smem_u32(base), bars = sb + Cfg::bars;
   auto bar = [&](int i) { return bars + 8u * i; };
-  float* tab = reinterpret_cast<float*>(base + Cfg::tab);  // tab[32 + n] = f1 l^n (0 for n < 0)
-  float* colf = tab + 64;                                  // weight of a block's column j at its edge
+  // Powers of l, made once: an exponential in the loop costs 20 instructions a thread.
+  float* pw = reinterpret_cast<float*>(base + Cfg::tab) + 32;  // pw[n] = l^n, -32 <= n <= 128 (0 for n < 0)
+  float* colf = pw + 136;                                      // weight of a block's column j at its edge
   uint32_t* taddr = reinterpret_cast<uint32_t*>(base + Cfg::taddr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LinearParams& P = Q.P;
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   if (threadIdx.x == 0) {
     if (sb & 1023u) record_error(LLSA_ERR_INTERNAL);  // the swizzle needs 1024-byte alignment
     for (int i = 0; i < kLtBars; ++i)
-      mbar_init(bar(i), i == kLtY || i == kLtP || i == kLtM || i == kLtOut ? Cfg::compute : 1);
+      mbar_init(bar(i), i == kLtY || i == kLtP || i == kLtM || i == kLtOut ? Cfg::compute / 32 : 1);
     mbar_fence_init();
   }
   if (warp == 4 * G + 1) {
@@ -201,11 +204,11 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   }
   pdl_wait();
   const float a = linear_decay(P.log_decay, h), a2 = a * kLog2e;
-  if (threadIdx.x < 64) {
+  if (threadIdx.x < 161) {
     const int n = (int)threadIdx.x - 32;
-    tab[threadIdx.x] = n < 0 ? 0.0f : R.f1 * exp2f(a2 * (float)n);
-  } else if (threadIdx.x < 96) {
-    const int j = (int)threadIdx.x - 64;
+    pw[n] = n < 0 ? 0.0f : exp2f(a2 * (float)n);
+  } else if (threadIdx.x < 193) {
+    const int j = (int)threadIdx.x - 161;
     colf[j] = exp2f(a2 * (float)(rev ? j : 31 - j));
   }
   lt_fence_before();
@@ -243,7 +246,13 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       }
       for (int c = 0; c < chunks; ++c) {
         if (OUT) {
-          // the chunk's products are done and its output is staged in X's place
+          // once the chunk's products are done Y and Z are free; X's place then holds its output
+          ok = mbar_wait(bar(kLtO), c & 1);
+          if (!ok) break;
+          if (c + 2 < chunks) {
+            load_yz(c + 2);
+            ++loaded;
+          }
           ok = mbar_wait(bar(kLtOut), c & 1);
           if (!ok) break;
           const uint32_t src = sb + (c & 1) * Cfg::stage + 2 * Cfg::tile;
@@ -251,12 +260,8 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           for (int g = 0; g < Cfg::subs; ++g)
             tma_store_3d(&Q.map[Q.iout[prob]], 64 * g, chunk_at(c), bh, src + g * Cfg::sub);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          if (c + 2 < chunks) load_yz(c + 2);
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          if (c + 2 < chunks) {
-            load(c + 2, &Q.map[Q.ix[prob]], 2);
-            ++loaded;
-          }
+          if (c + 2 < chunks) load(c + 2, &Q.map[Q.ix[prob]], 2);
         } else {
           ok = mbar_wait(bar(kLtT), c & 1);
           if (!ok) break;
@@ -337,6 +342,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     // this thread's 32 columns in a tile: four 16-byte pieces from `piece` on of sub-tile `tile_off`
     const int tile_off = (W * g / 64) * Cfg::sub, piece = (W * g % 64) / 8;
     auto wait = [&](int which, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(which), parity)); };
+    const float fall_chunk = expm1f(a * (float)C);
     float2 m[W / 2];                                   // columns 32 g .. of state row sr
     {
       const float* init = R.init ? R.init + (P.per_segment ? (long long)bh * P.nseg + seg : bh) * (D * D) : nullptr;
@@ -379,7 +385,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           *reinterpret_cast<uint4*>(y + Cfg::tile + at) = make_uint4(0, 0, 0, 0);
         }
       } else if (wants_state(c)) {
-        const float w1 = R.w * exp2f(a2 * (float)(rev ? i + 1 : n - 1 - i));
+        const float w1 = R.w * pw[rev ? i + 1 : n - 1 - i];
         const float2 w = make_float2(w1, w1), minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -398,7 +404,6 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           *reinterpret_cast<uint4*>(y2 + at) = make_uint4(two[0], two[1], two[2], two[3]);
         }
       }
-      __syncwarp();
       fence_proxy_async();
       lt_fence_before();
       lt_arrive(bar(kLtY));
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     // M + M (l^n - 1) + T rather than l^n M + T: a factor close to 1 repeated over thousands of
     // chunks would add up its rounding
     auto fold_t = [&](int c, int n) {
-      const float f1 = expm1f(a * (float)n);
+      const float f1 = n == C ? fall_chunk : expm1f(a * (float)n);
       const float2 fall = make_float2(f1, f1);
 #pragma unroll
       for (int e = 0; e < W; e += 16) {
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         for (int j = 0; j < 16; ++j) p[j] = 0u;
         return;
       }
-      const float e1 = R.f1 * exp2f(a2 * (float)(rev ? max(0, 32 * jb - i) : max(0, i - 32 * jb - 31)));
+      const float e1 = past < 0 ? R.f1 * pw[rev ? 32 * jb - i : i - 32 * jb - 31] : R.f1;
 #pragma unroll
       for (int q = 0; q < 32; q += 16) {
         uint32_t s[16];
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int dist = rev ? q + j - lane : lane - q - j;
-            const float w = tab[32 + dist];
+            const float w = pw[dist] * e1;
             s[j] = dist >= 0 ? __float_as_uint(__uint_as_float(s[j]) * w) : 0u;
           }
         }
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         lt_fence_after();
         weight_y(c, n);
         {
-          const float f1 = R.f2 * exp2f(a2 * (float)(rev ? max(0, n - 1 - i) : i + 1));
+          const float f1 = R.f2 * pw[rev ? max(0, n - 1 - i) : i + 1];
           const float2 f = make_float2(f1, f1);
 #pragma unroll
           for (int e = 0; e < W; e += 16) {
@@ -545,15 +550,15 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     if (R.state) {
       float* dst = R.state + (OUT ? (long long)bh : (long long)bh * P.nseg + seg) * (D * D) + sr * D + W * g;
       if (D == 64) {  // the two terms' halves meet in the copy's place, which no product reads now
-        float2* other = reinterpret_cast<float2*>(base + Cfg::mop) + (sr * D + W * g) / 2;
+        float2* other = reinterpret_cast<float2*>(base + Cfg::mop) + W / 2 * g * D + sr;  // [column pair][row]
         if (!first_term) {
 #pragma unroll
-          for (int e = 0; e < W / 2; ++e) other[e] = m[e];
+          for (int e = 0; e < W / 2; ++e) other[e * D] = m[e];
         }
         lt_bar(5, Cfg::compute);
         if (first_term) {
 #pragma unroll
-          for (int e = 0; e < W / 2; ++e) m[e] = make_float2(m[e].x + other[e].x, m[e].y + other[e].y);
+          for (int e = 0; e < W / 2; ++e) m[e] = make_float2(m[e].x + other[e * D].x, m[e].y + other[e * D].y);
         }
       }
       if (ok && first_term) {
