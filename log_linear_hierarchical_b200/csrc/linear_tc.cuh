@@ -21,7 +21,8 @@
 // Weights: l^{i-j} over a 32-column block of P is (l^{i - last column}) (l^{last column - j}), two
 // factors of at most 1, so one exponential a row and block serves 32 products and nothing
 // overflows for any decay.  The 32 x 32 blocks on the diagonal take l^{i-j} from a table by
-// distance; blocks past it are stored as zeros.
+// distance, whose other half is 0; blocks past it are stored as zeros.  (So a NaN among a chunk's
+// tokens reaches the chunk's other tokens, as through any tile of products.)
 //
 // Work split: a thread has one token row (a TMEM lane) and 32 of the D columns, so 8 warps at
 // D = 64, where two CTAs share an SM (112 KB of shared memory, 256 TMEM columns each), and 16 at
@@ -48,7 +49,7 @@ struct LtCfg {
   static constexpr int stage = (OUT ? 3 : 2) * tile;
   static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's second terms
   static constexpr int tab = mop + (OUT ? 1 : 2) * tile;
-  static constexpr int bars = tab + (32 + 136 + 32 + 8) * 4;
+  static constexpr int bars = tab + (136 + 32 + 64) * 4;
   static constexpr int taddr = bars + 10 * 8;
   static constexpr int smem = taddr + 16;
   // TMEM columns.  OUT at D = 64: P overlays the S columns of blocks 0 and 1 (both are in
@@ -107,14 +108,21 @@ __device__ __forceinline__ void lt_arrive(uint32_t bar) {
 #define LT_R8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
 #define LT_W8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
 
-// 16 columns of this warp's TMEM lanes, one lane a thread; the wait is part of it, so the
+// 32 columns of this warp's TMEM lanes, one lane a thread; the wait is part of it, so the
 // registers hold the values.
-__device__ __forceinline__ void lt_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void lt_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : LT_R8(r, 0), LT_R8(r, 8)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+      : LT_R8(r, 0), LT_R8(r, 8), LT_R8(r, 16), LT_R8(r, 24)
       : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void lt_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      LT_W8(r, 0), LT_W8(r, 8), LT_W8(r, 16), LT_W8(r, 24)
       : "memory");
 }
 __device__ __forceinline__ void lt_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -141,6 +149,13 @@ __device__ __forceinline__ float2 lt_fma2(float2 a, float2 b, float2 c) {
       : "=l"(reinterpret_cast<unsigned long long&>(d))
       : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
         "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 lt_add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
   return d;
 }
 __device__ __forceinline__ float2 lt_f2(uint32_t lo, uint32_t hi) {
@@ -178,8 +193,9 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   const uint32_t sb = smem_u32(base), bars = sb + Cfg::bars;
   auto bar = [&](int i) { return bars + 8u * i; };
   // Powers of l, made once: an exponential in the loop costs 20 instructions a thread.
-  float* pw = reinterpret_cast<float*>(base + Cfg::tab) + 32;  // pw[n] = l^n, -32 <= n <= 128 (0 for n < 0)
-  float* colf = pw + 136;                                      // weight of a block's column j at its edge
+  float* pw = reinterpret_cast<float*>(base + Cfg::tab);  // pw[n] = l^n, 0 <= n <= 128
+  float* colf = pw + 136;                                 // weight of a block's column j at its edge
+  float* diag = colf + 32;  // diag[32 + column - row] = f1 l^distance in a block on the diagonal, 0 past it
   uint32_t* taddr = reinterpret_cast<uint32_t*>(base + Cfg::taddr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LinearParams& P = Q.P;
@@ -204,12 +220,11 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   }
   pdl_wait();
   const float a = linear_decay(P.log_decay, h), a2 = a * kLog2e;
-  if (threadIdx.x < 161) {
-    const int n = (int)threadIdx.x - 32;
-    pw[n] = n < 0 ? 0.0f : exp2f(a2 * (float)n);
-  } else if (threadIdx.x < 193) {
-    const int j = (int)threadIdx.x - 161;
-    colf[j] = exp2f(a2 * (float)(rev ? j : 31 - j));
+  if (threadIdx.x < 129) pw[threadIdx.x] = exp2f(a2 * (float)threadIdx.x);
+  if (threadIdx.x >= 192 && threadIdx.x < 256) {
+    const int j = (int)threadIdx.x - 192, dist = rev ? j - 32 : 32 - j;
+    diag[j] = dist < 0 ? 0.0f : R.f1 * exp2f(a2 * (float)dist);
+    if (j < 32) colf[j] = exp2f(a2 * (float)(rev ? j : 31 - j));
   }
   lt_fence_before();
   __syncthreads();
@@ -413,19 +428,12 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     auto fold_t = [&](int c, int n) {
       const float f1 = n == C ? fall_chunk : expm1f(a * (float)n);
       const float2 fall = make_float2(f1, f1);
+      uint32_t t[W];
+      lt_ld32(tmem + lanes + Cfg::col_t + (OUT ? 0 : (c & 1) * D) + W * g, t);
 #pragma unroll
-      for (int e = 0; e < W; e += 16) {
-        uint32_t t[16];
-        lt_ld16(tmem + lanes + Cfg::col_t + (OUT ? 0 : (c & 1) * D) + W * g + e, t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float2& v = m[e / 2 + j];
-          const float2 d = lt_fma2(v, fall, v);
-          v = make_float2(d.x + __uint_as_float(t[2 * j]), d.y + __uint_as_float(t[2 * j + 1]));
-        }
-      }
+      for (int j = 0; j < W / 2; ++j) m[j] = lt_add2(lt_fma2(m[j], fall, m[j]), lt_f2(t[2 * j], t[2 * j + 1]));
     };
-    // 32 columns of P, in two halves
+    // 32 columns of P
     auto p_block = [&](int jb, int n, uint32_t (&p)[16]) {
       const int past = rev ? quarter - jb : jb - quarter;  // > 0: only masked pairs
       if (past > 0) {
@@ -433,35 +441,30 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         for (int j = 0; j < 16; ++j) p[j] = 0u;
         return;
       }
-      const float e1 = past < 0 ? R.f1 * pw[rev ? 32 * jb - i : i - 32 * jb - 31] : R.f1;
+      uint32_t s[32];
+      lt_ld32(tmem + lanes + Cfg::col_s + 32 * jb, s);
+      if (past < 0) {
+        const float e1 = R.f1 * pw[rev ? 32 * jb - i : i - 32 * jb - 31];
+        const float2 e = make_float2(e1, e1);
 #pragma unroll
-      for (int q = 0; q < 32; q += 16) {
-        uint32_t s[16];
-        lt_ld16(tmem + lanes + Cfg::col_s + 32 * jb + q, s);
-        if (past < 0) {
-          const float2 e = make_float2(e1, e1);
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 w = lt_mul2(*reinterpret_cast<const float2*>(colf + q + j), e);
-            const float2 v = lt_mul2(lt_f2(s[j], s[j + 1]), w);
-            s[j] = __float_as_uint(v.x);
-            s[j + 1] = __float_as_uint(v.y);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int dist = rev ? q + j - lane : lane - q - j;
-            const float w = pw[dist] * e1;
-            s[j] = dist >= 0 ? __float_as_uint(__uint_as_float(s[j]) * w) : 0u;
-          }
+        for (int j = 0; j < 32; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(colf + j);
+          const float2 u = lt_mul2(lt_f2(s[j], s[j + 1]), lt_mul2(make_float2(w.x, w.y), e));
+          const float2 v = lt_mul2(lt_f2(s[j + 2], s[j + 3]), lt_mul2(make_float2(w.z, w.w), e));
+          s[j] = __float_as_uint(u.x), s[j + 1] = __float_as_uint(u.y);
+          s[j + 2] = __float_as_uint(v.x), s[j + 3] = __float_as_uint(v.y);
         }
-        if (n < C) {  // columns behind the last token hold anything
+      } else {
+        const float* w = diag + 32 - lane;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[j] = 32 * jb + q + j < n ? s[j] : 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[q / 2 + j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * w[j]);
       }
+      if (n < C) {  // columns behind the last token hold anything
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j] = 32 * jb + j < n ? s[j] : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) p[j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
     };
     if (OUT) {
       store_m();
@@ -477,18 +480,15 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         {
           const float f1 = R.f2 * pw[rev ? max(0, n - 1 - i) : i + 1];
           const float2 f = make_float2(f1, f1);
+          uint32_t r[W];
+          lt_ld32(tmem + lanes + Cfg::col_o + W * g, r);
 #pragma unroll
-          for (int e = 0; e < W; e += 16) {
-            uint32_t r[16];
-            lt_ld16(tmem + lanes + Cfg::col_o + W * g + e, r);
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float2 v = lt_mul2(lt_f2(r[j], r[j + 1]), f);
-              r[j] = __float_as_uint(v.x);
-              r[j + 1] = __float_as_uint(v.y);
-            }
-            lt_st16(tmem + lanes + Cfg::col_o + W * g + e, r);
+          for (int j = 0; j < W; j += 2) {
+            const float2 v = lt_mul2(lt_f2(r[j], r[j + 1]), f);
+            r[j] = __float_as_uint(v.x);
+            r[j + 1] = __float_as_uint(v.y);
           }
+          lt_st32(tmem + lanes + Cfg::col_o + W * g, r);
         }
         uint32_t p[16];
         p_block(g, n, p);
@@ -512,13 +512,12 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         if (!ok) break;
         lt_fence_after();
         uint32_t o[16];
+        {
+          uint32_t r[W];
+          lt_ld32(tmem + lanes + Cfg::col_o + W * g, r);
 #pragma unroll
-        for (int e = 0; e < W; e += 16) {
-          uint32_t r[16];
-          lt_ld16(tmem + lanes + Cfg::col_o + W * g + e, r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[e / 2 + j] = i < n ? pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
+          for (int j = 0; j < 16; ++j)
+            o[j] = i < n ? pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
         }
         fence_proxy_async();
         lt_fence_before();
