@@ -70,9 +70,22 @@ struct alignas(64) LinearTcParams {
 // Shared-memory operand descriptors, 128-byte swizzle.  K-major: rows of 128 bytes, 8-row groups
 // `1024` apart.  MN-major: the 64 contiguous elements are M or N; 8-row groups of K are 1024
 // apart, 64-element groups of M or N `lbo` apart.
-__device__ __forceinline__ uint64_t lt_desc(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// The upper word is the same for all; the lower one is the address and lbo in 16-byte units, so
+// the steps through a tile are additions of constants.
+constexpr uint32_t kLtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t lt_desc(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4 << 16); }
+__device__ __forceinline__ uint64_t lt_desc64(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kLtDescHi));
+  return d;
+}
+
+// One thread of a converged warp.  (The products issued inside `if (lt_elect())` take the uniform
+// data path; from a divergent `lane == 0` branch each cost about 100 cycles to issue, more than most take.)
+__device__ __forceinline__ bool lt_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n .reg .b32 r;\n elect.sync r|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // kind::f16 instruction descriptor: fp32 accumulators, bf16 operands, MN-major flags.
@@ -81,17 +94,17 @@ __host__ __device__ constexpr uint32_t lt_idesc(int M, int N, int a_mn, int b_mn
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void lt_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void lt_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "l"(lt_desc64(a)), "l"(lt_desc64(b)), "r"(idesc), "r"(acc)
       : "memory");
 }
 // A from TMEM (bf16 pairs, one row a lane).
-__device__ __forceinline__ void lt_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void lt_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "r"(a), "l"(lt_desc64(b)), "r"(idesc), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void lt_commit(uint32_t bar) {
@@ -292,61 +305,66 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     }
   } else if (warp == 4 * G + 1) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t id_s = lt_idesc(128, 128, 0, 0), id_o = lt_idesc(128, D, 0, 1), id_t = lt_idesc(128, D, 1, 1);
-      constexpr uint32_t sub = Cfg::sub;
-      uint32_t last = 0, last_parity = 0;
-      auto commit = [&](int which, int c) {
-        lt_commit(bar(which));
-        last = bar(which), last_parity = c & 1;
-      };
-      for (int c = 0; c < chunks && ok; ++c) {
-        const uint32_t st = sb + (c & 1) * Cfg::stage;
-        const uint32_t y = st, z = st + Cfg::tile, x = st + 2 * Cfg::tile, m = sb + Cfg::mop;
-        if (OUT) {
-          ok = mbar_wait(bar(kLtFull + (c & 1)), (c >> 1) & 1) && mbar_wait(bar(kLtM), c & 1);
-          if (!ok) break;
-          lt_fence_after();
+    constexpr uint32_t id_s = lt_idesc(128, 128, 0, 0), id_o = lt_idesc(128, D, 0, 1), id_t = lt_idesc(128, D, 1, 1);
+    constexpr uint32_t sub = Cfg::sub;
+    auto wait = [&](int which, int parity) { ok = __all_sync(0xffffffffu, ok && mbar_wait(bar(which), parity)); };
+    auto k_major = [](int k) { return (k >> 2) * (sub >> 4) + (k & 3) * 2; };  // 16 channels on, in 16-byte units
+    auto mn_major = [](int k) { return k * 128; };                             // 16 rows on
+    int last = -1, last_parity = 0;
+    for (int c = 0; c < chunks && ok; ++c) {
+      const uint32_t y = sb + (c & 1) * Cfg::stage, z = y + Cfg::tile, x = y + 2 * Cfg::tile, m = sb + Cfg::mop;
+      if (OUT) {
+        wait(kLtFull + (c & 1), (c >> 1) & 1);
+        wait(kLtM, c & 1);
+        if (!ok) break;
+        lt_fence_after();
+        if (lt_elect()) {
+          const uint32_t dx = lt_desc(x, 16), dy = lt_desc(y, 16), dm = lt_desc(m, sub);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k >> 2) * sub + (k & 3) * 32;
-            lt_mma(tmem + Cfg::col_s, lt_desc(x + off, 16), lt_desc(y + off, 16), id_s, k > 0);
-          }
+          for (int k = 0; k < D / 16; ++k) lt_mma(tmem + Cfg::col_s, dx + k_major(k), dy + k_major(k), id_s, k > 0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {  // D = 64: X against the rows of both terms
-            const uint32_t off = (D == 64 ? 0 : (k >> 2) * sub) + (k & 3) * 32;
-            lt_mma(tmem + Cfg::col_o, lt_desc(x + off, 16), lt_desc(m + k * 2048, sub), id_o, k > 0);
-          }
-          commit(kLtS, c);
+          for (int k = 0; k < 8; ++k)  // D = 64: X against the rows of both terms
+            lt_mma(tmem + Cfg::col_o, dx + k_major(k & (D / 16 - 1)), dm + mn_major(k), id_o, k > 0);
+          lt_commit(bar(kLtS));
         }
-        if (wants_state(c)) {
-          ok = mbar_wait(bar(kLtY), c & 1);
-          if (!ok) break;
-          lt_fence_after();
-          const uint32_t y2 = OUT ? x : m + (c & 1) * Cfg::tile;
-          const uint32_t t = tmem + Cfg::col_t + (OUT ? 0 : (c & 1) * D);
+        __syncwarp();
+        last = kLtS, last_parity = c & 1;
+      }
+      if (wants_state(c)) {
+        wait(kLtY, c & 1);
+        if (!ok) break;
+        lt_fence_after();
+        const uint32_t y2 = OUT ? x : m + (c & 1) * Cfg::tile;
+        const uint32_t t = tmem + Cfg::col_t + (OUT ? 0 : (c & 1) * D);
+        if (lt_elect()) {
+          const uint32_t dy = lt_desc(y, D == 64 ? y2 - y : sub), dy2 = lt_desc(y2, sub), dz = lt_desc(z, sub);
 #pragma unroll
-          for (int k = 0; k < C / 16; ++k)
-            lt_mma(t, lt_desc(y + k * 2048, D == 64 ? y2 - y : sub), lt_desc(z + k * 2048, sub), id_t, k > 0);
+          for (int k = 0; k < C / 16; ++k) lt_mma(t, dy + mn_major(k), dz + mn_major(k), id_t, k > 0);
           if (D == 128) {
 #pragma unroll
-            for (int k = 0; k < C / 16; ++k)
-              lt_mma(t, lt_desc(y2 + k * 2048, sub), lt_desc(z + k * 2048, sub), id_t, 1);
+            for (int k = 0; k < C / 16; ++k) lt_mma(t, dy2 + mn_major(k), dz + mn_major(k), id_t, 1);
           }
-          commit(kLtT, c);
+          lt_commit(bar(kLtT));
         }
-        if (OUT) {
-          ok = mbar_wait(bar(kLtP), c & 1);
-          if (!ok) break;
-          lt_fence_after();
+        __syncwarp();
+        last = kLtT, last_parity = c & 1;
+      }
+      if (OUT) {
+        wait(kLtP, c & 1);
+        if (!ok) break;
+        lt_fence_after();
+        if (lt_elect()) {
+          const uint32_t dz = lt_desc(z, sub);
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)
-            lt_mma_ts(tmem + Cfg::col_o, tmem + Cfg::col_p + 8 * k, lt_desc(z + k * 2048, sub), id_o, 1);
-          commit(kLtO, c);
+            lt_mma_ts(tmem + Cfg::col_o, tmem + Cfg::col_p + 8 * k, dz + mn_major(k), id_o, 1);
+          lt_commit(bar(kLtO));
         }
+        __syncwarp();
+        last = kLtO, last_parity = c & 1;
       }
-      if (!ok && last) lt_drain(last, last_parity);
     }
+    if (!ok && last >= 0) lt_drain(bar(last), last_parity);
   } else {
     // ---------------------------------------------------------------- weights, state, output
     const int quarter = warp & 3, g = warp >> 2;
