@@ -49,17 +49,19 @@ struct LtCfg {
   static constexpr int stage = (OUT ? 3 : 2) * tile;
   static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's second terms
   static constexpr int tab = mop + (OUT ? 1 : 2) * tile;
-  static constexpr int bars = tab + (136 + 32 + 64) * 4;
-  static constexpr int taddr = bars + 10 * 8;
+  static constexpr int bars = tab + (132 + 32 + 64) * 4;
+  static constexpr int taddr = bars + 12 * 8;
   static constexpr int smem = taddr + 16;
-  // TMEM columns.  OUT at D = 64: P overlays the S columns of blocks 0 and 1 (both are in
-  // registers before either is overwritten).  Without OUT there are two T.
-  static constexpr uint32_t col_s = 0, col_o = 128, col_t = OUT ? 128 + D : 0;
-  static constexpr uint32_t col_p = D == 64 ? 0 : 384;
-  static constexpr uint32_t cols = OUT ? (D == 64 ? 256 : 512) : 2 * D;
+  // TMEM columns.  P overlays the S columns of blocks 0 and 1 (both are in registers before
+  // either is overwritten).  At D = 128 there are two O, so that a chunk's output leaves while the
+  // next chunk's X M runs; at D = 64 the other CTA of the SM fills that time.  Without OUT there
+  // are two T.
+  static constexpr bool defer = OUT && D == 128;
+  static constexpr uint32_t col_s = 0, col_p = 0, col_o = 128, col_t = OUT ? (defer ? 384 : 128 + D) : 0;
+  static constexpr uint32_t cols = OUT ? (defer ? 512 : 256) : 2 * D;
 };
 
-enum : int { kLtFull = 0, kLtS = 2, kLtY = 3, kLtT = 4, kLtP = 5, kLtO = 6, kLtM = 7, kLtOut = 8, kLtBars = 9 };
+enum : int { kLtFull = 0, kLtS = 2, kLtX, kLtY, kLtT, kLtP, kLtO, kLtM, kLtOut, kLtBars };
 
 struct alignas(64) LinearTcParams {
   CUtensorMap map[7];
@@ -196,6 +198,11 @@ __device__ __forceinline__ void lt_drain(uint32_t bar, uint32_t parity) {
     if (clock64() - t0 > kWaitLimitCycles / 2) return;
 }
 
+// 227 KB of an SM's 228 are for its CTAs, which each take 1 KB more than they ask for.
+static_assert(2 * (LtCfg<64, true>::smem + 1024) <= 228 * 1024 && 2 * (LtCfg<64, false>::smem + 1024) <= 228 * 1024 &&
+                  LtCfg<128, true>::smem <= 227 * 1024 && LtCfg<128, false>::smem <= 227 * 1024,
+              "shared memory of the CTAs that are to share an SM");
+
 template <int D, bool OUT>
 __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_per_sm)
     linear_tc_kernel(const __grid_constant__ LinearTcParams Q) {
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   auto bar = [&](int i) { return bars + 8u * i; };
   // Powers of l, made once: an exponential in the loop costs 20 instructions a thread.
   float* pw = reinterpret_cast<float*>(base + Cfg::tab);  // pw[n] = l^n, 0 <= n <= 128
-  float* colf = pw + 136;                                 // weight of a block's column j at its edge
+  float* colf = pw + 132;                                 // weight of a block's column j at its edge
   float* diag = colf + 32;  // diag[32 + column - row] = f1 l^distance in a block on the diagonal, 0 past it
   uint32_t* taddr = reinterpret_cast<uint32_t*>(base + Cfg::taddr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -262,25 +269,27 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         for (int g = 0; g < Cfg::subs; ++g)
           tma_load_4d(dst + g * Cfg::sub, m, 64 * g, chunk_at(c), h, b, bar(kLtFull + (c & 1)));
       };
-      auto load_yz = [&](int c) {
-        mbar_expect_tx(bar(kLtFull + (c & 1)), (OUT ? 3 : 2) * Cfg::tile);
-        load(c, &Q.map[Q.iy[prob]], 0);
-        load(c, &Q.map[Q.iz[prob]], 1);
-      };
+      auto expect = [&](int c) { mbar_expect_tx(bar(kLtFull + (c & 1)), (OUT ? 3 : 2) * Cfg::tile); };
       int loaded = 0;
       for (; loaded < min(2, chunks); ++loaded) {
-        load_yz(loaded);
+        expect(loaded);
+        load(loaded, &Q.map[Q.iy[prob]], 0);
         if (OUT) load(loaded, &Q.map[Q.ix[prob]], 2);
+        load(loaded, &Q.map[Q.iz[prob]], 1);
       }
-      for (int c = 0; c < chunks; ++c) {
-        if (OUT) {
-          // once the chunk's products are done Y and Z are free; X's place then holds its output
-          ok = mbar_wait(bar(kLtO), c & 1);
+      for (int c = 0; c < (OUT ? chunks : chunks - 2); ++c) {
+        const bool more = c + 2 < chunks;
+        if (more) {  // Y is free once T is formed, Z once O is
+          ok = mbar_wait(bar(kLtT), c & 1);
           if (!ok) break;
-          if (c + 2 < chunks) {
-            load_yz(c + 2);
-            ++loaded;
-          }
+          expect(c + 2);
+          ++loaded;
+          load(c + 2, &Q.map[Q.iy[prob]], 0);
+          if (OUT) ok = mbar_wait(bar(kLtO), c & 1);
+          if (!ok) break;
+          load(c + 2, &Q.map[Q.iz[prob]], 1);
+        }
+        if (OUT) {  // X's place holds the chunk's output
           ok = mbar_wait(bar(kLtOut), c & 1);
           if (!ok) break;
           const uint32_t src = sb + (c & 1) * Cfg::stage + 2 * Cfg::tile;
@@ -288,14 +297,9 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           for (int g = 0; g < Cfg::subs; ++g)
             tma_store_3d(&Q.map[Q.iout[prob]], 64 * g, chunk_at(c), bh, src + g * Cfg::sub);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          if (c + 2 < chunks) load(c + 2, &Q.map[Q.ix[prob]], 2);
-        } else {
-          ok = mbar_wait(bar(kLtT), c & 1);
-          if (!ok) break;
-          if (c + 2 < chunks) {
-            load_yz(c + 2);
-            ++loaded;
+          if (more) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            load(c + 2, &Q.map[Q.ix[prob]], 2);
           }
         }
       }
@@ -313,22 +317,32 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     int last = -1, last_parity = 0;
     for (int c = 0; c < chunks && ok; ++c) {
       const uint32_t y = sb + (c & 1) * Cfg::stage, z = y + Cfg::tile, x = y + 2 * Cfg::tile, m = sb + Cfg::mop;
+      const uint32_t o = tmem + Cfg::col_o + (Cfg::defer ? (c & 1) * D : 0);
       if (OUT) {
+        // S needs the last chunk's P read (its O complete); O needs M
+        const uint32_t dx = lt_desc(x, 16), dy = lt_desc(y, 16), dm = lt_desc(m, sub);
         wait(kLtFull + (c & 1), (c >> 1) & 1);
-        wait(kLtM, c & 1);
+        if (c > 0) wait(kLtO, (c - 1) & 1);
         if (!ok) break;
         lt_fence_after();
         if (lt_elect()) {
-          const uint32_t dx = lt_desc(x, 16), dy = lt_desc(y, 16), dm = lt_desc(m, sub);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) lt_mma(tmem + Cfg::col_s, dx + k_major(k), dy + k_major(k), id_s, k > 0);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)  // D = 64: X against the rows of both terms
-            lt_mma(tmem + Cfg::col_o, dx + k_major(k & (D / 16 - 1)), dm + mn_major(k), id_o, k > 0);
           lt_commit(bar(kLtS));
         }
         __syncwarp();
         last = kLtS, last_parity = c & 1;
+        wait(kLtM, c & 1);
+        if (!ok) break;
+        lt_fence_after();
+        if (lt_elect()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // D = 64: X against the rows of both terms
+            lt_mma(o, dx + k_major(k & (D / 16 - 1)), dm + mn_major(k), id_o, k > 0);
+          lt_commit(bar(kLtX));
+        }
+        __syncwarp();
+        last = kLtX, last_parity = c & 1;
       }
       if (wants_state(c)) {
         wait(kLtY, c & 1);
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           const uint32_t dz = lt_desc(z, sub);
 #pragma unroll
           for (int k = 0; k < C / 16; ++k)
-            lt_mma_ts(tmem + Cfg::col_o, tmem + Cfg::col_p + 8 * k, dz + mn_major(k), id_o, 1);
+            lt_mma_ts(o, tmem + Cfg::col_p + 8 * k, dz + mn_major(k), id_o, 1);
           lt_commit(bar(kLtO));
         }
         __syncwarp();
@@ -484,37 +498,61 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
 #pragma unroll
       for (int j = 0; j < 16; ++j) p[j] = pack_bf16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
     };
+    // A chunk's output, staged in X's place for the TMA warp
+    auto write_out = [&](int c) {
+      const int n = min(C, hi - chunk_at(c));
+      uint32_t r[W], o[16];
+      lt_ld32(tmem + lanes + Cfg::col_o + (Cfg::defer ? (c & 1) * D : 0) + W * g, r);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        o[j] = i < n ? pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
+      uint8_t* dst = base + (c & 1) * Cfg::stage + 2 * Cfg::tile + tile_off;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<uint4*>(dst + swz(i, piece + e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      fence_proxy_async();
+      lt_fence_before();
+      lt_arrive(bar(kLtOut));
+    };
     if (OUT) {
       store_m();
       fence_proxy_async();
       lt_arrive(bar(kLtM));
       for (int c = 0; c < chunks; ++c) {
         const int n = min(C, hi - chunk_at(c));
+        if (Cfg::defer && c > 0) {
+          wait(kLtO, (c - 1) & 1);
+          if (!ok) break;
+          lt_fence_after();
+          write_out(c - 1);
+        }
         wait(kLtFull + (c & 1), (c >> 1) & 1);  // this thread rewrites tokens that the copy brought in
         wait(kLtS, c & 1);
+        wait(kLtX, c & 1);
         if (!ok) break;
         lt_fence_after();
         weight_y(c, n);
+        uint32_t p[16];
+        p_block(g, n, p);
+        lt_bar(1 + quarter, 32 * G);  // S blocks 0 and 1 are read: P may overlay them
+        lt_st16(tmem + lanes + Cfg::col_p + 16 * g, p);
+        if (G == 2) {  // blocks 0 and 3 here, 1 and 2 there: at most two unmasked ones each
+          p_block(3 - g, n, p);
+          lt_st16(tmem + lanes + Cfg::col_p + 16 * (3 - g), p);
+        }
         {
           const float f1 = R.f2 * pw[rev ? max(0, n - 1 - i) : i + 1];
           const float2 f = make_float2(f1, f1);
+          const uint32_t at = tmem + lanes + Cfg::col_o + (Cfg::defer ? (c & 1) * D : 0) + W * g;
           uint32_t r[W];
-          lt_ld32(tmem + lanes + Cfg::col_o + W * g, r);
+          lt_ld32(at, r);
 #pragma unroll
           for (int j = 0; j < W; j += 2) {
             const float2 v = lt_mul2(lt_f2(r[j], r[j + 1]), f);
             r[j] = __float_as_uint(v.x);
             r[j + 1] = __float_as_uint(v.y);
           }
-          lt_st32(tmem + lanes + Cfg::col_o + W * g, r);
-        }
-        uint32_t p[16];
-        p_block(g, n, p);
-        if (G == 2) lt_bar(1 + quarter, 64);  // S blocks 0 and 1 are read: P may overlay them
-        lt_st16(tmem + lanes + Cfg::col_p + 16 * g, p);
-        if (G == 2) {  // blocks 0 and 3 here, 1 and 2 there: at most two unmasked ones each
-          p_block(3 - g, n, p);
-          lt_st16(tmem + lanes + Cfg::col_p + 16 * (3 - g), p);
+          lt_st32(at, r);
         }
         lt_wait_st();
         lt_fence_before();
@@ -526,29 +564,23 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           fold_t(c, n);
           if (c + 1 < chunks) store_m();
         }
-        wait(kLtO, c & 1);
-        if (!ok) break;
-        lt_fence_after();
-        uint32_t o[16];
-        {
-          uint32_t r[W];
-          lt_ld32(tmem + lanes + Cfg::col_o + W * g, r);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            o[j] = i < n ? pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])) : 0u;
+        if (!Cfg::defer) {
+          wait(kLtO, c & 1);
+          if (!ok) break;
+          lt_fence_after();
+          write_out(c);
         }
         fence_proxy_async();
         lt_fence_before();
         lt_arrive(bar(kLtM));
-        uint8_t* dst = base + (c & 1) * Cfg::stage + 2 * Cfg::tile + tile_off;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(dst + swz(i, piece + e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        fence_proxy_async();
-        lt_arrive(bar(kLtOut));
       }
-      // a warp that gave up releases the one it shares its lanes with, whose next wait gives up too
-      if (G == 2 && !ok) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");
+      if (Cfg::defer && ok && chunks > 0) {
+        wait(kLtO, (chunks - 1) & 1);
+        lt_fence_after();
+        if (ok) write_out(chunks - 1);
+      }
+      // a warp that gave up releases those that it shares its lanes with, whose next wait gives up too
+      if (!ok) asm volatile("bar.arrive %0, %1;" ::"r"(1 + quarter), "n"(32 * G) : "memory");
     } else {
       for (int c = 0; c <= chunks; ++c) {
         if (c < chunks) {
