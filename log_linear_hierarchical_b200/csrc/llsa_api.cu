@@ -3,6 +3,7 @@
 // is one module global per device.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 #include <new>
 
@@ -1021,10 +1022,28 @@ LinearStream linear_stream(const llsa_linear_shape* s, const void* p, const int6
   return LinearStream{p, st[0], st[1], st[2]};
 }
 
+// allow_smem for a kernel that is launched often: asked for once per device.  The calling
+// thread's context is made current first (encoding a tensor map needs one, and a thread whose
+// first CUDA call this is, such as an autograd worker, has none).
+template <auto Kern>
+bool allow_smem_once(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};
+  thread_local int bound = -1;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (bound != dev && cudaSetDevice(dev) != cudaSuccess) return false;
+  bound = dev;
+  const unsigned long long bit = dev < 64 ? 1ULL << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (!allow_smem(Kern, bytes)) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 template <typename T, int D, bool OUT>
 llsa_status linear_simt_launch(const LinearParams& P, int bh, cudaStream_t cs) {
   const int smem = linear_simt_smem<D>(OUT);
-  if (!allow_smem(linear_simt_kernel<T, D, OUT>, smem)) return LLSA_ERR_CUDA;
+  if (!allow_smem_once<linear_simt_kernel<T, D, OUT>>(smem)) return LLSA_ERR_CUDA;
   const long long ctas = (long long)bh * P.nseg * P.nprob;
   if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
   return launch(OUT ? kKLinearChunk : kKLinearState, cs, [&] {
@@ -1063,7 +1082,7 @@ bool make_out_map(CUtensorMap* m, void* out, int BH, int N, int D) {
 template <int D, bool OUT>
 llsa_status linear_tc_launch(const llsa_linear_shape* s, const LinearParams& P, cudaStream_t cs) {
   using Cfg = LtCfg<D, OUT>;
-  if (!allow_smem(linear_tc_kernel<D, OUT>, Cfg::smem)) return LLSA_ERR_CUDA;
+  if (!allow_smem_once<linear_tc_kernel<D, OUT>>(Cfg::smem)) return LLSA_ERR_CUDA;
   LinearTcParams Q{};
   Q.P = P;
   int used = 0;

@@ -3,13 +3,14 @@ _step (include/llsa.h) and the autograd op."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
 from ._lib import LLSALinearShape
-from .api import _DTYPES, LLSAError, _check, _p, _stream
-from .rotary import _on_device, _torch_stream
+from .api import _DTYPES, LLSAError, _check, _stream
+from .rotary import _current_stream, _on_device, _torch_stream
 
 
 def make_linear_shape(B: int, H: int, N: int, D: int, dtype, scale: float | None = None) -> LLSALinearShape:
@@ -31,25 +32,36 @@ def llsa_linear_workspace_bytes(shape: LLSALinearShape) -> int:
     return _lib.load().llsa_linear_workspace_bytes(ctypes.byref(shape))
 
 
+@functools.lru_cache(maxsize=1024)
+def _sizes(B: int, H: int, N: int, D: int, code: int) -> tuple[int, int, int]:
+    """(status, states elements, workspace bytes) of a shape, which need no device to ask."""
+    ref = ctypes.byref(LLSALinearShape(B, H, N, D, code, 1.0))
+    lib = _lib.load()
+    return lib.llsa_linear_validate(ref), lib.llsa_linear_states_elems(ref), lib.llsa_linear_workspace_bytes(ref)
+
+
 def _tokens(shape, t: torch.Tensor, name: str, strides) -> int:
-    """Address of a [B, H, N, D] input whose strides (written to ``strides``) the kernels take."""
-    want = (shape.B, shape.H, shape.N, shape.D)
-    if tuple(t.shape) != want:
-        raise ValueError(f"{name}: {tuple(t.shape)}, but the shape is {want}")
+    """Address of a [B, H, N, D] input whose strides (written to ``strides``; zeros stand for
+    contiguous) the kernels take."""
+    if t.shape != (shape.B, shape.H, shape.N, shape.D):
+        raise ValueError(f"{name}: {tuple(t.shape)}, but the shape is {(shape.B, shape.H, shape.N, shape.D)}")
     if _DTYPES.get(t.dtype) != shape.dtype:
         raise ValueError(f"{name}: dtype {t.dtype} is not the shape's")
     _on_device(t, name)
     if not _readable(t):
         raise ValueError(f"{name}: strides {t.stride()} or alignment not taken (see include/llsa.h); make it contiguous")
-    strides[:] = t.stride()[:3]
+    strides[:] = (0, 0, 0) if t.is_contiguous() else t.stride()[:3]
     return t.data_ptr()
 
 
 def _readable(t: torch.Tensor) -> bool:
     """Whether the kernels read this view in place: channels contiguous, rows of whole 16 bytes."""
+    if t.data_ptr() % 16:
+        return False
+    if t.is_contiguous():
+        return True
     per16 = 16 // t.element_size()
-    return (t.stride(3) == 1 and t.data_ptr() % 16 == 0
-            and all(n == 1 or (s > 0 and s % per16 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])))
+    return t.stride(3) == 1 and all(n == 1 or (s > 0 and s % per16 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
 
 
 def _laid_out(t: torch.Tensor) -> torch.Tensor:
@@ -63,7 +75,13 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
 def _output(shape, t: torch.Tensor, name: str) -> int:
     if _DTYPES.get(t.dtype) != shape.dtype or t.numel() != shape.B * shape.H * shape.N * shape.D:
         raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, but the shape needs B*H*N*D elements of its dtype")
-    return _p(t, name)
+    return _address(t, name)
+
+
+def _address(t: torch.Tensor, name: str) -> int:
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: LLSA buffers must be contiguous")
+    return _on_device(t, name).data_ptr()
 
 
 def _f32(t: torch.Tensor | None, need: int, name: str) -> int | None:
@@ -71,7 +89,7 @@ def _f32(t: torch.Tensor | None, need: int, name: str) -> int | None:
         return None
     if t.dtype != torch.float32 or t.numel() < need:
         raise ValueError(f"{name}: {t.numel()} elements of {t.dtype}, expected {need} of float32")
-    return _p(t, name)
+    return _address(t, name)
 
 
 def _i32(t: torch.Tensor | None, need: int, name: str) -> int | None:
@@ -79,7 +97,7 @@ def _i32(t: torch.Tensor | None, need: int, name: str) -> int | None:
         return None
     if t.dtype != torch.int32 or t.numel() != need:
         raise ValueError(f"{name}: {t.numel()} elements of {t.dtype}, expected {need} of int32")
-    return _p(t, name)
+    return _address(t, name)
 
 
 def _states(shape) -> int:
@@ -89,40 +107,40 @@ def _states(shape) -> int:
 def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None, initial_state=None,
                         final_state=None, stream=None) -> None:
     sd = _states(shape)
+    stream = _current_stream(q) if stream is None else _stream(stream)
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
             _tokens(shape, v, "v", shape.v_strides), _f32(log_decay, shape.H, "log_decay"),
             _i32(lengths, shape.B, "lengths"), _f32(initial_state, sd, "initial_state"), _output(shape, o, "o"),
-            _f32(final_state, sd, "final_state"), _f32(states, llsa_linear_states_elems(shape), "states")]
-    _check("llsa_linear_forward", _lib.load().llsa_linear_forward(ctypes.byref(shape), *args, _stream(stream)))
+            _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states")]
+    _check("llsa_linear_forward", _lib.load().llsa_linear_forward(ctypes.byref(shape), *args, stream))
 
 
 def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None, workspace=None, lengths=None,
                          initial_state=None, d_final=None, d_initial=None, stream=None) -> None:
     sd = _states(shape)
+    stream = _current_stream(q) if stream is None else _stream(stream)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
             _tokens(shape, v, "v", shape.v_strides), _tokens(shape, do, "do", shape.dO_strides),
             _f32(log_decay, shape.H, "log_decay"), _i32(lengths, shape.B, "lengths"),
             _f32(initial_state, sd, "initial_state"), _f32(d_final, sd, "d_final"),
-            _f32(states, llsa_linear_states_elems(shape), "states"), _output(shape, dq, "dq"),
+            _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states"), _output(shape, dq, "dq"),
             _output(shape, dk, "dk"), _output(shape, dv, "dv"), _f32(d_initial, sd, "d_initial"),
-            _p(workspace, "workspace")]
-    _check("llsa_linear_backward", _lib.load().llsa_linear_backward(ctypes.byref(shape), *args, nbytes,
-                                                                    _stream(stream)))
+            None if workspace is None else _address(workspace, "workspace")]
+    _check("llsa_linear_backward", _lib.load().llsa_linear_backward(ctypes.byref(shape), *args, nbytes, stream))
 
 
 def _forward(q, k, v, log_decay, scale, initial_state, lengths, want_state):
     if q.dim() != 4 or q.dtype not in _DTYPES:
         raise ValueError(f"q: {tuple(q.shape)} {q.dtype}, expected [B, H, N, D] of bfloat16 or float32")
     shape = make_linear_shape(*q.shape, q.dtype, scale)
-    st = llsa_linear_validate(shape)
+    st, n, _ = _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)
     if st != 0:
         raise LLSAError("llsa_linear_validate", st)
-    dev = q.device
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    final = torch.empty(shape.B, shape.H, shape.D, shape.D, device=dev) if want_state else None
-    n = llsa_linear_states_elems(shape)
-    states = torch.empty(n, device=dev) if n else None
+    _on_device(q, "q")
+    o = q.new_empty(q.shape)
+    final = q.new_empty((shape.B, shape.H, shape.D, shape.D), dtype=torch.float32) if want_state else None
+    states = q.new_empty(n, dtype=torch.float32) if n else None
     llsa_linear_forward(shape, q, k, v, log_decay, o, states, lengths, initial_state, final)
     return shape, o, final, states
 
@@ -140,16 +158,15 @@ class _LinearAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, d_final=None):
         q, k, v, log_decay, initial_state, lengths, states = ctx.saved_tensors
-        none = (None,) * 8
         if do is None and d_final is None:
-            return none
+            return (None,) * 8
         shape = make_linear_shape(*q.shape, q.dtype, ctx.scale)
-        do = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if do is None else _laid_out(do)
+        do = q.new_zeros(q.shape) if do is None else _laid_out(do)
         d_final = None if d_final is None else _dense(d_final)
-        dq, dk, dv = (torch.empty(q.shape, dtype=q.dtype, device=q.device) for _ in range(3))
+        dq, dk, dv = q.new_empty((3, *q.shape)).unbind(0)
         d_initial = torch.empty_like(initial_state) if ctx.needs_input_grad[5] else None
-        n = llsa_linear_workspace_bytes(shape)
-        workspace = torch.empty((n + 3) // 4, device=q.device) if n else None
+        n = _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[2]
+        workspace = q.new_empty(n // 4, dtype=torch.float32) if n else None
         llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states, workspace, lengths, initial_state,
                              d_final, d_initial)
         return dq, dk, dv, None, None, d_initial, None, None
@@ -207,8 +224,8 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
         raise ValueError(f"pool: {tuple(pool.shape)} {pool.dtype}, expected [P, {H}, {D}, {D}] of float32")
     shape = make_linear_shape(B, H, 1, D, q.dtype, scale)
     q, k, v = _dense(q), _dense(k), _dense(v)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
-    args = [_p(q, "q"), _p(k, "k"), _p(v, "v"), _f32(log_decay, H, "log_decay"), _p(pool, "pool"),
+    o = q.new_empty(q.shape) if out is None else out
+    args = [_address(q, "q"), _address(k, "k"), _address(v, "v"), _f32(log_decay, H, "log_decay"), _address(pool, "pool"),
             pool.shape[0], _i32(slots, B, "slots"), _i32(out_slots, B, "out_slots"), _output(shape, o, "out")]
-    _check("llsa_linear_step", _lib.load().llsa_linear_step(ctypes.byref(shape), *args, _stream(None)))
+    _check("llsa_linear_step", _lib.load().llsa_linear_step(ctypes.byref(shape), *args, _current_stream(q)))
     return o

@@ -55,9 +55,15 @@ def _on_device(t: torch.Tensor, name: str) -> torch.Tensor:
     """A CUDA tensor on the current device (the kernels read and write its address)."""
     if not t.is_cuda:
         raise ValueError(f"{name}: LLSA buffers must be CUDA tensors (the kernels read device memory)")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return t
+
+
+def _current_stream(t: torch.Tensor) -> int:
+    """The current stream of t's device as an address (without torch.cuda's wrapper object, which
+    costs as much as a launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _torch_stream(stream) -> torch.cuda.Stream:
@@ -75,12 +81,16 @@ def _heads(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
     return _on_device(t, name)
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse, stream) -> list:
     """One launch over one or two tensors; ``outs`` None makes new contiguous ones."""
     x = xs[0]
     B, H, N, D = x.shape
-    for i, t in enumerate(xs):
-        _heads(t, ("q", "k")[i], x)
+    _heads(x, "q", x)
+    if len(xs) == 2:
+        _heads(xs[1], "k", x)
     if frequencies.dtype != torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous():
         raise ValueError("frequencies: expected a contiguous 1-D float64 tensor, one value for each pair")
     _on_device(frequencies, "frequencies")
@@ -99,15 +109,16 @@ def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse
             flags |= _lib.LLSA_ROTARY_POSITIONS_I32
     xs = [t if t.stride(-1) == 1 else t.contiguous() for t in xs]
     if outs is None:
-        outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs]
+        outs = [t.new_empty(t.shape) for t in xs]
     two = len(xs) == 2
+    stream = _current_stream(x) if stream is None else _stream(stream)
     shape = LLSARotaryShape(B, H, xs[1].shape[1] if two else 0, N, D, _DTYPES[x.dtype], 2 * frequencies.numel(),
                             first, flags, scale)
-    strides = [(ctypes.c_int64 * 3)(*t.stride()[:3]) for t in xs]
+    strides = [None if t.is_contiguous() else _Strides(*t.stride()[:3]) for t in xs]
     _check("llsa_rotary", _lib.load().llsa_rotary(
         ctypes.byref(shape), xs[0].data_ptr(), strides[0], xs[1].data_ptr() if two else None,
         strides[1] if two else None, pos, pos_stride, frequencies.data_ptr(), outs[0].data_ptr(),
-        outs[1].data_ptr() if two else None, _stream(stream)))
+        outs[1].data_ptr() if two else None, stream))
     return outs
 
 
