@@ -452,7 +452,7 @@ llsa_status llsa_rotary(const llsa_rotary_shape* shape, const void* x, const int
  * segments that the sequence is cut into start.
  * Arithmetic: bf16 inputs use bf16 tensor-core products with fp32 accumulation; fp32 inputs use fp32
  * throughout; states are fp32.  The results do not depend on timing (no atomics).
- * Rules: B, H, N >= 1; D == 64 or 128; B * H * N < 2^31; H <= 65535.
+ * Rules: B, H, N >= 1; D == 64 or 128; B * H * N < 2^31; N <= 2^30; H <= 65535.
  */
 typedef struct {
   int32_t B, H, N, D;

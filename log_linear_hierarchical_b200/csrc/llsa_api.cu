@@ -990,7 +990,7 @@ llsa_status linear_validate(const llsa_linear_shape* s) {
       if (dims[d] > 1 && (st[d] <= 0 || st[d] % per16 != 0 || st[d] >= (1LL << 36))) return LLSA_ERR_INVALID_ARG;
   }
   if (s->D != 64 && s->D != 128) return LLSA_ERR_UNSUPPORTED;
-  if (s->H > 65535 || (long long)s->B * s->H >= (1LL << 31) || (long long)s->B * s->H * s->N >= (1LL << 31))
+  if (s->N > (1 << 30) || s->H > 65535 || (long long)s->B * s->H >= (1LL << 31) || (long long)s->B * s->H * s->N >= (1LL << 31))
     return LLSA_ERR_UNSUPPORTED;
   return LLSA_OK;
 }
