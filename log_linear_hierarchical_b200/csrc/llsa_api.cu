@@ -8,7 +8,8 @@
 #include <new>
 
 #include "attn_simt.cuh"
-#include "linear_simt.cuh"
+#include "linear_f32.cuh"
+#include "linear_scan.cuh"
 #include "linear_step.cuh"
 #include "linear_tc.cuh"
 #include "probe.cuh"
@@ -1040,14 +1041,14 @@ bool allow_smem_once(size_t bytes) {
   return true;
 }
 
-template <typename T, int D, bool OUT>
-llsa_status linear_simt_launch(const LinearParams& P, int bh, cudaStream_t cs) {
-  const int smem = linear_simt_smem<D>(OUT);
-  if (!allow_smem_once<linear_simt_kernel<T, D, OUT>>(smem)) return LLSA_ERR_CUDA;
+template <int D, bool OUT>
+llsa_status linear_f32_launch(const LinearParams& P, int bh, cudaStream_t cs) {
+  const int smem = linear_f32_smem<D>(OUT);
+  if (!allow_smem_once<linear_f32_kernel<D, OUT>>(smem)) return LLSA_ERR_CUDA;
   const long long ctas = (long long)bh * P.nseg * P.nprob;
   if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
   return launch(OUT ? kKLinearChunk : kKLinearState, cs, [&] {
-    launch_pdl(linear_simt_kernel<T, D, OUT>, dim3((unsigned)ctas), dim3(kLsThreads), smem, cs, P);
+    launch_pdl(linear_f32_kernel<D, OUT>, dim3((unsigned)ctas), dim3(kLfThreads), smem, cs, P);
   });
 }
 
@@ -1116,7 +1117,7 @@ llsa_status linear_pass(const llsa_linear_shape* s, const LinearParams& P, cudaS
   const int bh = s->B * s->H;
   if (s->dtype == LLSA_BF16)
     return s->D == 64 ? linear_tc_launch<64, OUT>(s, P, cs) : linear_tc_launch<128, OUT>(s, P, cs);
-  return s->D == 64 ? linear_simt_launch<float, 64, OUT>(P, bh, cs) : linear_simt_launch<float, 128, OUT>(P, bh, cs);
+  return s->D == 64 ? linear_f32_launch<64, OUT>(P, bh, cs) : linear_f32_launch<128, OUT>(P, bh, cs);
 }
 
 // Segment states of the streams (y, z) of `P.p[0]` (its first pass), then the scan.
