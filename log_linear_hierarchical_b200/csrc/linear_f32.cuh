@@ -3,7 +3,7 @@
 // tokens taken from the segment's end).
 //
 // Products run on the tensor cores with fp32 accuracy: each factor is split into two TF32 terms,
-// x = hi + lo (hi: x rounded to TF32; lo = x - hi exactly, of which TF32 keeps 11 bits), and
+// x = hi + lo (hi: x with its low 13 bits cleared; lo = x - hi exactly, of which TF32 keeps 11 bits), and
 // lo hi + hi lo + hi hi of 8 channels at a time are formed on the tensor cores, smallest first, and
 // added to the sums on the FP32 pipes: the tensor cores' own additions cut off instead of
 // rounding, which over a chunk's sums cost 1.3e-6 of the result instead of 2e-7.  mma.sync m16n8k8 does 509 multiply-adds a cycle and SM here, so three of them
@@ -37,8 +37,7 @@ struct LfPair {
   uint32_t hi, lo;
 };
 __device__ __forceinline__ LfPair lf_split(float x) {
-  uint32_t hi;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
   return LfPair{hi, __float_as_uint(x - __uint_as_float(hi))};
 }
 
@@ -46,6 +45,12 @@ __device__ __forceinline__ void lf_mma(float (&d)[4], const uint32_t (&a)[4], ui
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same without an addend.
+__device__ __forceinline__ void lf_mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Fragments of one k step: A (rows r, r + 8; columns k, k + 4) and B (rows k, k + 4; column n).
@@ -63,8 +68,8 @@ struct LfA {
 };
 __device__ __forceinline__ void lf_mma3(float (&d)[4], const LfA& a, float b0, float b1) {
   const LfPair p = lf_split(b0), q = lf_split(b1);
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
-  lf_mma(t, a.lo, p.hi, q.hi);
+  float t[4];
+  lf_mma0(t, a.lo, p.hi, q.hi);
   lf_mma(t, a.hi, p.lo, q.lo);
   lf_mma(t, a.hi, p.hi, q.hi);
 #pragma unroll
@@ -126,17 +131,27 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
       *reinterpret_cast<float4*>(dst + r * D + (c ^ lf_swz(r))) = v;
     }
   };
-  // Fragment reads.  Eight rows from r0 on (a multiple of 8), columns k and k + 4 on: the row's
-  // permutation is lf_swz(fr) whatever r0, so element (r0 + fr, k + fc) is at row_at(..) + (k ^ f24) and
-  // (.., k + 4 + fc) at row_at4(..) + (k ^ f24).
-  const int f24 = lf_swz(fr) & 24, f4 = lf_swz(fr) & 4;
-  auto row_at = [&](const float* t, int ld, int r0) { return t + (r0 + fr) * ld + (fc ^ f4); };
-  auto row_at4 = [&](const float* t, int ld, int r0) { return t + (r0 + fr) * ld + (fc ^ f4 ^ 4); };
-  // Rows k + fc and k + 4 + fc (k a multiple of 8), column c0 + fr (c0 a multiple of 8): the permutation
-  // is that of rows fc and fc + 4.
+  // Fragment reads.  The permutations depend on fr or fc alone, so every address is a pointer made once
+  // for each of four neighbouring 8-column groups plus a constant.
+  // Eight rows from r0 on (a multiple of 8), columns 8g and 8g + 4 on: row_at(.., g % 4)[32 * (g / 4)] is element
+  // (r0 + fr, 8g + fc), and (.., 8g + 4 + fc) with `half` 4.
+  const int fs = lf_swz(fr), f24 = fs & 24;
+  auto row_at = [&](const float* t, int ld, int r0, int g, int half) {
+    return t + (r0 + fr) * ld + ((8 * g) ^ f24) + (fc ^ (fs & 4) ^ half);
+  };
+  // Rows k + fc (and k + 4 + fc with `half` 4), k a multiple of 8, columns c0 + 8g on (c0 a multiple of 32):
+  // col_at(.., g % 4)[k * D + 32 * (g / 4)].
   const int cx = fc << 3;
-  auto col_at = [&](const float* t, int c0) { return t + fc * D + (c0 ^ cx) + fr; };
-  auto col_at4 = [&](const float* t, int c0) { return t + (fc + 4) * D + (c0 ^ cx) + (fr ^ 4); };
+  auto col_at = [&](const float* t, int c0, int g, int half) {
+    return t + (fc + half) * D + c0 + ((8 * g) ^ cx) + (fr ^ half);
+  };
+  const float *zp[4], *zq[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    zp[g] = col_at(sz, wc * (D / 2), g, 0);
+    zq[g] = col_at(sz, wc * (D / 2), g, 4);
+  }
+  constexpr int kMinusZ = OUT ? C * D + 3 * C + 8 + C * D + C * C : 0;  // sm - sz
 
   for (int done = 0; done < hi - lo; done += C) {
     const int n = min(C, hi - lo - done);
@@ -153,22 +168,30 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
     __syncthreads();
     float acc[NT][4];  // output rows 16 wr .., columns wc D/2 ..
     if (OUT) {
-      const float *x0 = row_at(sx, D, 16 * wr), *x4 = row_at4(sx, D, 16 * wr);
+      const float *x0[4], *x4[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        x0[g] = row_at(sx, D, 16 * wr, g, 0);
+        x4[g] = row_at(sx, D, 16 * wr, g, 4);
+      }
       // P = f1 l^{i-j} X Y^T: rows 16 wr .., every other 8-column tile (wc, wc + 2, ..), none past the diagonal
       float p[4][4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[u][e] = 0.0f;
-      const float *y0 = row_at(sy, D, 8 * wc), *y4 = row_at4(sy, D, 8 * wc);
-#pragma unroll 2
-      for (int k = 0; k < D; k += 8) {
-        LfA x;
-        const int kk = k ^ f24;
-        x.set(x0[kk], x0[8 * D + kk], x4[kk], x4[8 * D + kk]);
+      const int to_y = (int)(row_at(sy, D, 8 * wc, 0, 0) - x0[0]);
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (u <= wr) lf_mma3(p[u], x, y0[16 * u * D + kk], y4[16 * u * D + kk]);
+        for (int g = 0; g < 4; ++g) {
+          LfA x;
+          x.set(x0[g][k], x0[g][k + 8 * D], x4[g][k], x4[g][k + 8 * D]);
+          const float *y0 = x0[g] + to_y + k, *y4 = x4[g] + to_y + k;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (u <= wr) lf_mma3(p[u], x, y0[16 * u * D], y4[16 * u * D]);
+        }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -185,14 +208,17 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[u][e] = 0.0f;
 #pragma unroll 1
-      for (int k = 0; k < D; k += 8) {
-        LfA x;
-        const int kk = k ^ f24;
-        x.set(x0[kk], x0[8 * D + kk], x4[kk], x4[8 * D + kk]);
-        const float* t = sm + k * D;
+      for (int k = 0; k < D; k += 32) {
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-          lf_mma3(acc[u], x, *col_at(t, wc * (D / 2) + 8 * u), *col_at4(t, wc * (D / 2) + 8 * u));
+        for (int g = 0; g < 4; ++g) {
+          LfA x;
+          x.set(x0[g][k], x0[g][k + 8 * D], x4[g][k], x4[g][k + 8 * D]);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int off = kMinusZ + (k + 8 * g) * D + 32 * (u >> 2);
+            lf_mma3(acc[u], x, zp[u & 3][off], zq[u & 3][off]);
+          }
+        }
       }
       const float w0 = Q.f2 * wx[16 * wr + fr], w1 = Q.f2 * wx[16 * wr + fr + 8];
 #pragma unroll
@@ -205,16 +231,20 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
       __syncthreads();  // the products are written, the state's copy has been read
       // + P Z, up to the diagonal and the last token
       const int last = min(n, 16 * wr + 16);
-      const float *p0 = row_at(sp, C, 16 * wr), *p4 = row_at4(sp, C, 16 * wr);
 #pragma unroll 1
-      for (int k = 0; k < last; k += 8) {
-        LfA q;
-        const int kk = k ^ f24;
-        q.set(p0[kk], p0[8 * C + kk], p4[kk], p4[8 * C + kk]);
-        const float* t = sz + k * D;
+      for (int k = 0; k < last; k += 16) {  // (rows behind the last token are zeros)
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-          lf_mma3(acc[u], q, *col_at(t, wc * (D / 2) + 8 * u), *col_at4(t, wc * (D / 2) + 8 * u));
+        for (int g = 0; g < 2; ++g) {
+          LfA q;
+          const float *p0 = row_at(sp, C, 16 * wr, ((k >> 3) & 3) + g, 0) + (k & 32),
+                      *p4 = row_at(sp, C, 16 * wr, ((k >> 3) & 3) + g, 4) + (k & 32);
+          q.set(p0[0], p0[8 * C], p4[0], p4[8 * C]);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int off = (k + 8 * g) * D + 32 * (u >> 2);
+            lf_mma3(acc[u], q, zp[u & 3][off], zq[u & 3][off]);
+          }
+        }
       }
       float* out = static_cast<float*>(Q.out) + (long long)bh * P.N * D + wc * (D / 2) + 2 * fc;
 #pragma unroll
@@ -240,16 +270,22 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[u][e] = 0.0f;
       const int r0 = wr * (D / 4) + 16 * i;
-      const float *ya = col_at(sy, r0), *yb = col_at(sy, r0 + 8), *ya4 = col_at4(sy, r0), *yb4 = col_at4(sy, r0 + 8);
+      const float *ya = col_at(sy, r0 & ~31, (r0 & 31) / 8, 0), *yb = col_at(sy, r0 & ~31, (r0 & 31) / 8 + 1, 0),
+                  *ya4 = col_at(sy, r0 & ~31, (r0 & 31) / 8, 4), *yb4 = col_at(sy, r0 & ~31, (r0 & 31) / 8 + 1, 4);
 #pragma unroll 1
-      for (int k = 0; k < n; k += 8) {
-        LfA y;
-        const float w0 = wy[k + fc], w1 = wy[k + 4 + fc];
-        y.set(w0 * ya[k * D], w0 * yb[k * D], w1 * ya4[k * D], w1 * yb4[k * D]);
-        const float* z = sz + k * D;
+      for (int k = 0; k < n; k += 16) {
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
-          lf_mma3(t[u], y, *col_at(z, wc * (D / 2) + 8 * u), *col_at4(z, wc * (D / 2) + 8 * u));
+        for (int g = 0; g < 2; ++g) {
+          LfA y;
+          const int kr = k + 8 * g;
+          const float w0 = wy[kr + fc], w1 = wy[kr + 4 + fc];
+          y.set(w0 * ya[kr * D], w0 * yb[kr * D], w1 * ya4[kr * D], w1 * yb4[kr * D]);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) {
+            const int off = kr * D + 32 * (u >> 2);
+            lf_mma3(t[u], y, zp[u & 3][off], zq[u & 3][off]);
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < NT; ++u)
