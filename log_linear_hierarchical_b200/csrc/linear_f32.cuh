@@ -20,7 +20,6 @@
 
 namespace llsa {
 
-constexpr int kLfThreads = 256;
 constexpr int kLfChunk = 64;
 
 template <int D>
@@ -78,9 +77,11 @@ __device__ __forceinline__ void lf_mma3(float (&d)[4], const LfA& a, float b0, f
 
 // OUT: the outputs and the state; otherwise only the state (the first pass over segments).
 template <int D, bool OUT>
-__global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel(const LinearParams P) {
+__global__ void __launch_bounds__(4 * D, D == 64 ? 2 : 1) linear_f32_kernel(const LinearParams P) {
   constexpr int C = kLfChunk;
-  constexpr int MT = D / 64, NT = D / 16;  // a warp's tiles of the state: D / 4 rows, D / 2 columns
+  constexpr int T = 4 * D;                 // threads: 4 warps along the rows, WC along the columns
+  constexpr int WC = D / 32;
+  constexpr int MT = D / 64, NT = 4;       // a warp's tiles of the state: D / 4 rows, 32 columns
   extern __shared__ float4 lf_smem[];
   float* sy = reinterpret_cast<float*>(lf_smem);
   float* sz = sy + C * D;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
   float* sm = sp + (OUT ? C * C : 0);
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wr = warp >> 1, wc = warp & 1;  // rows and columns of this warp: quarters by halves
+  const int wr = warp / WC, wc = warp % WC;
   const int fr = lane >> 2, fc = lane & 3;  // fragment row and column
   const int prob = blockIdx.x % P.nprob;
   const int s = (blockIdx.x / P.nprob) % P.nseg, bh = blockIdx.x / P.nprob / P.nseg;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
   const int lo = s * P.seg, top = min(P.N, lo + P.seg), hi = max(lo, min(top, len));
   if (tid <= C) pw[tid] = exp2f(a2 * (float)tid);
 
-  // the state: rows wr D/4 .. of M, columns wc D/2 .., as accumulator fragments
+  // the state: rows wr D/4 .. of M, columns 32 wc .., as accumulator fragments
   float m[MT][NT][4];
   const float* init = Q.init ? Q.init + (P.per_segment ? (long long)bh * P.nseg + s : bh) * (D * D) : nullptr;
   auto each_m = [&](auto&& f) {
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
       for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          f(m[t][u][e], wr * (D / 4) + 16 * t + fr + 8 * (e >> 1), wc * (D / 2) + 8 * u + 2 * fc + (e & 1));
+          f(m[t][u][e], wr * (D / 4) + 16 * t + fr + 8 * (e >> 1), 32 * wc + 8 * u + 2 * fc + (e & 1));
   };
   each_m([&](float& v, int r, int c) { v = init ? __ldg(init + (Q.transpose ? c * D + r : r * D + c)) : 0.0f; });
   auto copy_m = [&]() {
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
   auto load_tile = [&](const LinearStream& S, float* dst, int base, int n) {
     const float* src = static_cast<const float*>(S.p) + b * S.sb + h * S.sh;
 #pragma unroll
-    for (int i = tid; i < C * (D / 4); i += kLfThreads) {
+    for (int i = tid; i < C * (D / 4); i += T) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < n) v = __ldg(reinterpret_cast<const float4*>(src + (long long)(Q.rev ? base - r : base + r) * S.sn + c));
@@ -132,15 +133,15 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
     }
   };
   // Fragment reads.  The permutations depend on fr or fc alone, so every address is a pointer made once
-  // for each of four neighbouring 8-column groups plus a constant.
+  // for each of four neighbouring 8-column groups, and a constant.
   // Eight rows from r0 on (a multiple of 8), columns 8g and 8g + 4 on: row_at(.., g % 4)[32 * (g / 4)] is element
   // (r0 + fr, 8g + fc), and (.., 8g + 4 + fc) with `half` 4.
   const int fs = lf_swz(fr), f24 = fs & 24;
   auto row_at = [&](const float* t, int ld, int r0, int g, int half) {
     return t + (r0 + fr) * ld + ((8 * g) ^ f24) + (fc ^ (fs & 4) ^ half);
   };
-  // Rows k + fc (and k + 4 + fc with `half` 4), k a multiple of 8, columns c0 + 8g on (c0 a multiple of 32):
-  // col_at(.., g % 4)[k * D + 32 * (g / 4)].
+  // Rows k + fc (and k + 4 + fc with `half` 4), k a multiple of 8, columns c0 + 8g on (c0 a multiple of 32,
+  // g < 4): col_at(.., g)[k * D].
   const int cx = fc << 3;
   auto col_at = [&](const float* t, int c0, int g, int half) {
     return t + (fc + half) * D + c0 + ((8 * g) ^ cx) + (fr ^ half);
@@ -148,8 +149,8 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
   const float *zp[4], *zq[4];
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    zp[g] = col_at(sz, wc * (D / 2), g, 0);
-    zq[g] = col_at(sz, wc * (D / 2), g, 4);
+    zp[g] = col_at(sz, 32 * wc, g, 0);
+    zq[g] = col_at(sz, 32 * wc, g, 4);
   }
   constexpr int kMinusZ = OUT ? C * D + 3 * C + 8 + C * D + C * C : 0;  // sm - sz
 
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
       wx[tid] = pw[tid + e];
     }
     __syncthreads();
-    float acc[NT][4];  // output rows 16 wr .., columns wc D/2 ..
+    float acc[NT][4];  // output rows 16 wr .., columns 32 wc ..
     if (OUT) {
       const float *x0[4], *x4[4];
 #pragma unroll
@@ -174,10 +175,11 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
         x0[g] = row_at(sx, D, 16 * wr, g, 0);
         x4[g] = row_at(sx, D, 16 * wr, g, 4);
       }
-      // P = f1 l^{i-j} X Y^T: rows 16 wr .., every other 8-column tile (wc, wc + 2, ..), none past the diagonal
-      float p[4][4];
+      // P = f1 l^{i-j} X Y^T: rows 16 wr .., 8-column tiles wc, wc + WC, .., none past the diagonal
+      constexpr int PT = 8 / WC;
+      float p[PT][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < PT; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[u][e] = 0.0f;
       const int to_y = (int)(row_at(sy, D, 8 * wc, 0, 0) - x0[0]);
@@ -189,16 +191,16 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
           x.set(x0[g][k], x0[g][k + 8 * D], x4[g][k], x4[g][k + 8 * D]);
           const float *y0 = x0[g] + to_y + k, *y4 = x4[g] + to_y + k;
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (u <= wr) lf_mma3(p[u], x, y0[16 * u * D], y4[16 * u * D]);
+          for (int u = 0; u < PT; ++u)
+            if (wc + WC * u < 2 * wr + 2) lf_mma3(p[u], x, y0[8 * WC * u * D], y4[8 * WC * u * D]);
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u <= wr) {
+      for (int u = 0; u < PT; ++u)
+        if (wc + WC * u < 2 * wr + 2) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = 16 * wr + fr + 8 * (e >> 1), j = 8 * (2 * u + wc) + 2 * fc + (e & 1);
+            const int i = 16 * wr + fr + 8 * (e >> 1), j = 8 * (WC * u + wc) + 2 * fc + (e & 1);
             sp[i * C + (j ^ lf_swz(i))] = j <= i ? p[u][e] * (Q.f1 * pw[i - j]) : 0.0f;
           }
         }
@@ -215,8 +217,8 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
           x.set(x0[g][k], x0[g][k + 8 * D], x4[g][k], x4[g][k + 8 * D]);
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            const int off = kMinusZ + (k + 8 * g) * D + 32 * (u >> 2);
-            lf_mma3(acc[u], x, zp[u & 3][off], zq[u & 3][off]);
+            const int off = kMinusZ + (k + 8 * g) * D;
+            lf_mma3(acc[u], x, zp[u][off], zq[u][off]);
           }
         }
       }
@@ -241,12 +243,12 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
           q.set(p0[0], p0[8 * C], p4[0], p4[8 * C]);
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            const int off = (k + 8 * g) * D + 32 * (u >> 2);
-            lf_mma3(acc[u], q, zp[u & 3][off], zq[u & 3][off]);
+            const int off = (k + 8 * g) * D;
+            lf_mma3(acc[u], q, zp[u][off], zq[u][off]);
           }
         }
       }
-      float* out = static_cast<float*>(Q.out) + (long long)bh * P.N * D + wc * (D / 2) + 2 * fc;
+      float* out = static_cast<float*>(Q.out) + (long long)bh * P.N * D + 32 * wc + 2 * fc;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int i = 16 * wr + fr + 8 * e;
@@ -282,8 +284,8 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
           y.set(w0 * ya[kr * D], w0 * yb[kr * D], w1 * ya4[kr * D], w1 * yb4[kr * D]);
 #pragma unroll
           for (int u = 0; u < NT; ++u) {
-            const int off = kr * D + 32 * (u >> 2);
-            lf_mma3(t[u], y, zp[u & 3][off], zq[u & 3][off]);
+            const int off = kr * D;
+            lf_mma3(t[u], y, zp[u][off], zq[u][off]);
           }
         }
       }
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kLfThreads, D == 64 ? 2 : 1) linear_f32_kernel
   }
   if (OUT) {  // rows that take no part
     float4* out = reinterpret_cast<float4*>(static_cast<float*>(Q.out) + ((long long)bh * P.N + hi) * D);
-    for (long long i = tid; i < (long long)(top - hi) * (D / 4); i += kLfThreads) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (long long i = tid; i < (long long)(top - hi) * (D / 4); i += T) out[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   if (Q.state) {
     float* dst = Q.state + (OUT ? (long long)bh : (long long)bh * P.nseg + s) * (D * D);

@@ -1048,7 +1048,7 @@ llsa_status linear_f32_launch(const LinearParams& P, int bh, cudaStream_t cs) {
   const long long ctas = (long long)bh * P.nseg * P.nprob;
   if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
   return launch(OUT ? kKLinearChunk : kKLinearState, cs, [&] {
-    launch_pdl(linear_f32_kernel<D, OUT>, dim3((unsigned)ctas), dim3(kLfThreads), smem, cs, P);
+    launch_pdl(linear_f32_kernel<D, OUT>, dim3((unsigned)ctas), dim3(4 * D), smem, cs, P);
   });
 }
 
