@@ -439,19 +439,25 @@ llsa_status llsa_rotary(const llsa_rotary_shape* shape, const void* x, const int
  * q, k, v (and dO): [B, H, N, D] `dtype`, 16-byte aligned, channels contiguous; strides of
  * batch, head and token in elements, all three 0 for contiguous, each a positive number of
  * whole 16 bytes (the stride of a dimension of size 1 is not looked at).  o, dq, dk, dv:
- * [B, H, N, D] contiguous, not overlapping the inputs.
+ * [B, H, N, D] contiguous.
  * log_decay: [H] fp32, natural logarithms, normally <= 0 (0: no decay; -infinity: only the
  * token itself).  Values above 0 grow without bound and are the caller's risk.
  * lengths: [B] int32 or NULL (every row has N tokens).  Positions at or past lengths[b] take
  * no part whatever they hold: their o, dq, dk, dv are 0 and the final state is the state after
  * lengths[b] tokens (0 tokens: the initial state).  A length outside [0, N] is clamped and
  * recorded as LLSA_ERR_INTERNAL in the device status word.
- * initial_state, final_state and their gradients: [B, H, D, D] fp32 or NULL.
+ * initial_state, final_state and their gradients: [B, H, D, D] fp32 or NULL.  final_state may be
+ * initial_state itself; every other overlap of an output with an input or another output is
+ * refused (LLSA_ERR_INVALID_ARG).
  * states: caller-owned scratch of llsa_linear_states_elems(shape) fp32 elements (NULL when that
  * is 0) that llsa_linear_forward fills and llsa_linear_backward reads: the states at which the
  * segments that the sequence is cut into start.
- * Arithmetic: bf16 inputs use bf16 tensor-core products with fp32 accumulation; fp32 inputs use fp32
- * throughout; states are fp32.  The results do not depend on timing (no atomics).
+ * Arithmetic: bf16 inputs use bf16 tensor-core products with fp32 accumulation (the masked
+ * products and the state's copy that q meets are rounded to bf16, the tokens that enter the state
+ * keep 16 bits); fp32 inputs use products of two TF32 terms a factor (relative error about 2^-21)
+ * and fp32 sums; states are fp32.  The results do not depend on timing (no atomics).  Tokens are
+ * taken in chunks of 128 (fp32: 64): a NaN or infinity at a token may reach every output of its
+ * chunk, the earlier ones too.
  * Rules: B, H, N >= 1; D == 64 or 128; B * H * N < 2^31; N <= 2^30; H <= 65535.
  */
 typedef struct {
@@ -489,9 +495,10 @@ llsa_status llsa_linear_backward(const llsa_linear_shape* shape, const void* q, 
  * tokens of one call).  pool: [pool_rows, H, D, D] fp32.  slots: [B] int32 or NULL (row b uses
  * slot b); out_slots: [B] int32 or NULL (the state is updated in place).  Different slots
  * keep the old state, for a token that may be rejected.  A row with a negative slot takes no
- * part: its o is 0.  A row whose slot is not in the pool, or that would write a slot which an
- * earlier taking-part row reads or writes or read one which such a row writes, takes no part
- * either and is recorded as LLSA_ERR_INTERNAL.  Without slots, B <= pool_rows.
+ * part: its o is 0 and nothing else is written.  A row with a slot that is not in the pool, or
+ * that would race with an earlier row whose slots are (one of the two writes a slot that the
+ * other reads or writes), takes no part either and is recorded as LLSA_ERR_INTERNAL.  Without
+ * slots, B <= pool_rows.  o and the pool overlap no input and not each other.
  */
 llsa_status llsa_linear_step(const llsa_linear_shape* shape, const void* q, const void* k, const void* v,
                              const float* log_decay, float* pool, int32_t pool_rows, const int32_t* slots,

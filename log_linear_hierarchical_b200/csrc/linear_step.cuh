@@ -27,16 +27,17 @@ struct StepParams {
   float scale;
 };
 
-// Rows whose slot is negative take no part (o = 0).  A slot outside the pool, or one that an
-// earlier row writes or reads while this row writes it (the two would race), is recorded as
-// LLSA_ERR_INTERNAL and the row takes no part either, so the first row with a slot has it.
+// Rows with a negative slot take no part (o = 0).  A row with a slot outside the pool, or that
+// would race with an earlier row of valid slots (one of the two writes what the other reads or
+// writes), is recorded as LLSA_ERR_INTERNAL and takes no part either, so the first row with a
+// slot has it.
 __device__ __forceinline__ bool step_row_allowed(const StepParams& P, int b, int in, int out) {
   bool bad = false;
   if (P.slots || P.out_slots)
     for (int r = threadIdx.x; r < b; r += kStepThreads) {
       const int i = P.slots ? __ldg(P.slots + r) : r;
       const int o = P.out_slots ? __ldg(P.out_slots + r) : i;
-      if (i >= 0 && o >= 0) bad = bad || o == out || o == in || i == out;
+      if (i >= 0 && o >= 0 && i < P.pool_rows && o < P.pool_rows) bad = bad || o == out || o == in || i == out;
     }
   bad = __syncthreads_or(bad);
   if (in < 0 || out < 0) return false;

@@ -1156,6 +1156,43 @@ LinearParams linear_params(const llsa_linear_shape* s, const float* log_decay, c
 
 bool aligned_or_null(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// The bytes that a call reads and writes, to refuse outputs that overlap anything else.
+struct Overlaps {
+  Extent in[8], out[5];
+  int nin = 0, nout = 0;
+  bool bad = false;
+  void input(const llsa_linear_shape* s, const void* p, const int64_t (&given)[3]) {
+    long long st[3];
+    strides_or_contiguous(given, s->H, s->N, s->D, st);
+    bad = bad || !extent_of(p, s->B, s->H, s->N, s->D, st, dtype_bytes(s->dtype), &in[nin++]);
+  }
+  void input(const void* p, size_t bytes) {
+    if (p) in[nin++] = span(p, bytes);
+  }
+  void output(const void* p, size_t bytes) {
+    if (p) out[nout++] = span(p, bytes);
+  }
+  bool any() const {
+    for (int i = 0; i < nout; ++i) {
+      for (int j = 0; j < nin; ++j)
+        if (out[i].overlaps(in[j])) return true;
+      for (int j = 0; j < i; ++j)
+        if (out[i].overlaps(out[j])) return true;
+    }
+    return bad;
+  }
+
+ private:
+  static Extent span(const void* p, size_t bytes) {
+    return Extent{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes};
+  }
+};
+
+size_t linear_token_bytes(const llsa_linear_shape* s) {
+  return (size_t)s->B * s->H * s->N * s->D * dtype_bytes(s->dtype);
+}
+size_t linear_state_bytes(const llsa_linear_shape* s) { return (size_t)s->B * s->H * s->D * s->D * sizeof(float); }
+
 }  // namespace
 
 extern "C" {
@@ -1437,6 +1474,15 @@ llsa_status llsa_linear_forward(const llsa_linear_shape* s, const void* q, const
       !aligned16(final_state) || !aligned16(states))
     return LLSA_ERR_INVALID_ARG;
   if (need && !states) return LLSA_ERR_WORKSPACE;
+  Overlaps lap;
+  lap.input(s, q, s->q_strides);
+  lap.input(s, k, s->k_strides);
+  lap.input(s, v, s->v_strides);
+  if (initial_state != final_state) lap.input(initial_state, linear_state_bytes(s));
+  lap.output(o, linear_token_bytes(s));
+  lap.output(final_state, linear_state_bytes(s));
+  if (need) lap.output(states, need * sizeof(float));
+  if (lap.any()) return LLSA_ERR_INVALID_ARG;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LinearParams P = linear_params(s, log_decay, lengths);
   LinearProblem& Q = P.p[0];
@@ -1471,6 +1517,18 @@ llsa_status llsa_linear_backward(const llsa_linear_shape* s, const void* q, cons
       !aligned16(d_final) || !aligned16(d_initial) || !aligned16(states) || !aligned16(workspace))
     return LLSA_ERR_INVALID_ARG;
   if (need && (!states || !workspace || workspace_bytes < need * sizeof(float))) return LLSA_ERR_WORKSPACE;
+  Overlaps lap;
+  lap.input(s, q, s->q_strides);
+  lap.input(s, k, s->k_strides);
+  lap.input(s, v, s->v_strides);
+  lap.input(s, dO, s->dO_strides);
+  lap.input(initial_state, linear_state_bytes(s));
+  lap.input(d_final, linear_state_bytes(s));
+  if (need) lap.input(states, need * sizeof(float));
+  for (const void* p : {dq, dk, dv}) lap.output(p, linear_token_bytes(s));
+  lap.output(d_initial, linear_state_bytes(s));
+  if (need) lap.output(workspace, need * sizeof(float));
+  if (lap.any()) return LLSA_ERR_INVALID_ARG;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const LinearStream sq = linear_stream(s, q, s->q_strides), sk = linear_stream(s, k, s->k_strides),
                      sv = linear_stream(s, v, s->v_strides), sd = linear_stream(s, dO, s->dO_strides);
@@ -1501,6 +1559,14 @@ llsa_status llsa_linear_step(const llsa_linear_shape* s, const void* q, const vo
   if (!log_decay || !aligned_or_null(log_decay, 4) || !aligned_or_null(slots, 4) || !aligned_or_null(out_slots, 4))
     return LLSA_ERR_INVALID_ARG;
   if (pool_rows < 1 || (!slots && s->B > pool_rows)) return LLSA_ERR_INVALID_ARG;
+  Overlaps lap;
+  for (const void* p : {q, k, v}) lap.input(p, linear_token_bytes(s));
+  lap.input(log_decay, s->H * sizeof(float));
+  lap.input(slots, s->B * sizeof(int32_t));
+  lap.input(out_slots, s->B * sizeof(int32_t));
+  lap.output(o, linear_token_bytes(s));
+  lap.output(pool, (size_t)pool_rows * s->H * s->D * s->D * sizeof(float));
+  if (lap.any()) return LLSA_ERR_INVALID_ARG;
   const long long ctas = (long long)s->B * s->H * (s->D / 32);
   if (ctas >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
   const StepParams P{q, k, v, o, log_decay, pool, slots, out_slots, s->B, s->H, pool_rows, s->scale};

@@ -186,6 +186,9 @@ def llsa_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     take no part and get 0.  ``return_state``: returns (o, state after the last token), which
     ``llsa_linear_step`` or the next call's ``initial_state`` carries on from.
 
+    A NaN or infinity at a token may reach the earlier outputs of its chunk of 128 tokens (fp32: 64).
+    Before a backward pass is captured into a CUDA graph, drop eager graphs of the same leaves (torch
+    ties a leaf's gradient to the stream that the leaf was first used on).
     Views whose rows are whole 16-byte pieces (a [B, N, H, D] projection transposed) are read in
     place; others are copied first."""
     if log_decay.requires_grad and torch.is_grad_enabled():

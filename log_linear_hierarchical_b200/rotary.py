@@ -9,7 +9,7 @@ import torch
 
 from . import _lib
 from ._lib import LLSARotaryShape
-from .api import _DTYPES, _check, _stream
+from .api import _DTYPES, _check
 
 
 def llsa_rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -84,7 +84,7 @@ def _heads(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
 _Strides = ctypes.c_int64 * 3
 
 
-def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse, stream) -> list:
+def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse) -> list:
     """One launch over one or two tensors; ``outs`` None makes new contiguous ones."""
     x = xs[0]
     B, H, N, D = x.shape
@@ -111,7 +111,7 @@ def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse
     if outs is None:
         outs = [t.new_empty(t.shape) for t in xs]
     two = len(xs) == 2
-    stream = _current_stream(x) if stream is None else _stream(stream)
+    stream = _current_stream(x)
     shape = LLSARotaryShape(B, H, xs[1].shape[1] if two else 0, N, D, _DTYPES[x.dtype], 2 * frequencies.numel(),
                             first, flags, scale)
     strides = [None if t.is_contiguous() else _Strides(*t.stride()[:3]) for t in xs]
@@ -127,8 +127,7 @@ class _Rotary(torch.autograd.Function):
     def forward(ctx, q, k, positions, frequencies, interleaved, first, scale):
         ctx.set_materialize_grads(False)
         ctx.args = (positions, frequencies, interleaved, first, scale)
-        outs = _rotate([q] if k is None else [q, k], None, positions, frequencies, interleaved, first, scale, False,
-                       None)
+        outs = _rotate([q] if k is None else [q, k], None, positions, frequencies, interleaved, first, scale, False)
         return outs[0] if k is None else tuple(outs)
 
     @staticmethod
@@ -138,8 +137,7 @@ class _Rotary(torch.autograd.Function):
         there = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
         back = [None, None]
         if there:
-            outs = _rotate([grads[i] for i in there], None, positions, frequencies, interleaved, first, scale, True,
-                           None)
+            outs = _rotate([grads[i] for i in there], None, positions, frequencies, interleaved, first, scale, True)
             for i, o in zip(there, outs):
                 back[i] = o
         return (*back, None, None, None, None, None)
@@ -158,9 +156,12 @@ def llsa_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
     2c + 1), and multiplied by ``scale``; the others are copied.  Gradients reach q and k by the
     inverse rotation (under grad, on the current stream).  ``inplace`` (contiguous tensors, no
     gradients): q and k themselves are overwritten and returned."""
-    if stream is not None and not inplace:  # new tensors belong to the stream that writes them
+    if stream is not None:  # copies and new tensors belong to the stream that uses them
         with torch.cuda.stream(_torch_stream(stream)):
-            return llsa_rotary(q, k, positions, frequencies, interleaved=interleaved, first=first, scale=scale)
+            return llsa_rotary(q, k, positions, frequencies, interleaved=interleaved, first=first, scale=scale,
+                               inplace=inplace)
+    if frequencies.requires_grad and torch.is_grad_enabled():
+        raise ValueError("frequencies get no gradient: pass them detached")
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
         if inplace:
             raise ValueError("inplace is for calls without gradients")
@@ -168,5 +169,5 @@ def llsa_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
     xs = [q] if k is None else [q, k]
     if inplace and not all(t.is_contiguous() for t in xs):
         raise ValueError("inplace needs contiguous tensors")
-    outs = _rotate(xs, xs if inplace else None, positions, frequencies, interleaved, first, scale, False, stream)
+    outs = _rotate(xs, xs if inplace else None, positions, frequencies, interleaved, first, scale, False)
     return outs[0] if k is None else tuple(outs)
