@@ -947,9 +947,10 @@ llsa_status rotary_launch(const llsa_rotary_shape* s, const void* x, const int64
     const bool in_place = in[i] == out[i] && is_contiguous(s->B, heads[i], s->N, s->D, st);
     if (!in_place && ein[i].overlaps(eout[i])) return LLSA_ERR_INVALID_ARG;
     const int dims[3] = {s->B, heads[i], s->N};
-    for (int d = 0; d < 3; ++d) vec = vec && (dims[d] == 1 || (st[d] * (long long)e) % 16 == 0);
-    vec = vec && aligned16(in[i]) && aligned16(out[i]);
-    P.t[i] = RotaryTensor{in[i], out[i], st[0], st[1], st[2], heads[i]};
+    bool x_vec = aligned16(in[i]);
+    for (int d = 0; d < 3; ++d) x_vec = x_vec && (dims[d] == 1 || (st[d] * (long long)e) % 16 == 0);
+    vec = vec && x_vec && aligned16(out[i]);
+    P.t[i] = RotaryTensor{in[i], out[i], st[0], st[1], st[2], heads[i], x_vec, aligned16(out[i])};
   }
   if (P.tensors == 2 && (eout[0].overlaps(eout[1]) || ein[0].overlaps(eout[1]) || ein[1].overlaps(eout[0])))
     return LLSA_ERR_INVALID_ARG;
@@ -965,19 +966,29 @@ llsa_status rotary_launch(const llsa_rotary_shape* s, const void* x, const int64
   P.pos_stride = position_stride;
   P.freq = frequencies;
   P.scale = s->scale;
-  const long long units = vec ? s->D / 16 : s->rot / 2 + (s->D - s->rot);
-  const long long blocks = ((long long)s->B * s->N * units + kRotThreads - 1) / kRotThreads;
+  const long long rows = (long long)s->B * s->N;
+  const long long blocks = vec ? (rows * (s->D / 16) + kRotThreads - 1) / kRotThreads : (rows + kAnyRows - 1) / kAnyRows;
   if (blocks >= (1LL << 31)) return LLSA_ERR_UNSUPPORTED;
-  // heads of one thread: all of them (the angles are computed once) unless that leaves fewer
-  // than four CTAs for each SM; then as many CTAs along the heads as fill them
-  const long long want = (4LL * kSms + blocks - 1) / blocks;
+  // heads of one thread or CTA: all of them (the angles are computed once) unless that leaves fewer
+  // than eight CTAs for each SM; then as many CTAs along the heads as fill them
+  const long long want = (8LL * kSms + blocks - 1) / blocks;
   const int split = (int)(want < Hmax ? want : Hmax);
   P.heads = (Hmax + split - 1) / split;
   const dim3 grid((unsigned)blocks, (unsigned)((Hmax + P.heads - 1) / P.heads));
   if (grid.y > 65535) return LLSA_ERR_UNSUPPORTED;
-  auto kern = s->dtype == LLSA_BF16 ? (vec ? rotary_vec_kernel<__nv_bfloat16> : rotary_pair_kernel<__nv_bfloat16>)
-                                    : (vec ? rotary_vec_kernel<float> : rotary_pair_kernel<float>);
-  return launch(kKRotary, cs, [&] { launch_pdl(kern, grid, dim3(kRotThreads), 0, cs, P); });
+  if (vec) {
+    auto kern = s->dtype == LLSA_BF16 ? rotary_vec_kernel<__nv_bfloat16> : rotary_vec_kernel<float>;
+    return launch(kKRotary, cs, [&] { launch_pdl(kern, grid, dim3(kRotThreads), 0, cs, P); });
+  }
+  auto any = [&](auto kern, int smem) -> llsa_status {
+    return launch(kKRotary, cs, [&] { launch_pdl(kern, grid, dim3(kRotThreads), smem, cs, P); });
+  };
+  const int pairs = s->rot / 2;  // (48 KB of shared memory at most: no attribute to set)
+  if (s->dtype == LLSA_BF16)
+    return s->D == 64 ? any(rotary_any_kernel<__nv_bfloat16, 64>, rotary_any_smem<__nv_bfloat16, 64>(pairs))
+                      : any(rotary_any_kernel<__nv_bfloat16, 128>, rotary_any_smem<__nv_bfloat16, 128>(pairs));
+  return s->D == 64 ? any(rotary_any_kernel<float, 64>, rotary_any_smem<float, 64>(pairs))
+                    : any(rotary_any_kernel<float, 128>, rotary_any_smem<float, 128>(pairs));
 }
 
 llsa_status linear_validate(const llsa_linear_shape* s) {

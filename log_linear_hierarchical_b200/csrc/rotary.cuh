@@ -27,6 +27,7 @@ struct RotaryTensor {
   void* y;               // [B, H, N, D] contiguous
   long long sb, sh, sn;  // strides of x in elements (channels are contiguous)
   int H;
+  int x_vec, y_vec;      // rows are 16-byte aligned
 };
 
 struct RotaryParams {
@@ -208,54 +209,110 @@ __global__ void __launch_bounds__(kRotThreads) rotary_vec_kernel(const RotaryPar
   }
 }
 
-// Any even rot and first, any element alignment: one pair, or one copied channel, per thread.
-constexpr int kPairAhead = 4;
+// Any even rot and first, any element alignment.  A CTA takes kAnyRows token rows and goes through its
+// heads: a head's rows come into shared memory in 16-byte pieces (element by element where the tensor
+// is not aligned to them), the pairs are turned there with angles from a table made once, and the
+// rows leave the same way; the next head's pieces are on their way meanwhile.  (65536 tokens, 6 heads
+// of 64 bf16 channels, q and k, 46 of them turned from channel 8 on; a thread for each pair, reading
+// and writing global memory 2 bytes at a time, took 111 us.)
+constexpr int kAnyRows = 32;
 
-template <typename T>
-__global__ void __launch_bounds__(kRotThreads) rotary_pair_kernel(const RotaryParams P) {
+template <typename T, int D>
+constexpr int rotary_any_smem(int pairs) {
+  return kAnyRows * (pairs * 8 + D * (int)sizeof(T) + 4 * 8);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotaryParams P) {
+  constexpr int E = 16 / (int)sizeof(T), row_pieces = D / E, pieces = kAnyRows * row_pieces / kRotThreads;
+  extern __shared__ float4 any_smem[];
+  T* tile = reinterpret_cast<T*>(any_smem);                             // [kAnyRows][D]
+  long long* from = reinterpret_cast<long long*>(tile + kAnyRows * D);  // [2][kAnyRows] row offsets of x
+  long long* to = from + 2 * kAnyRows;                                  // and of y
+  float2* turn = reinterpret_cast<float2*>(to + 2 * kAnyRows);          // [kAnyRows][pairs] cos, sin
   pdl_enter();
-  const int pairs = P.rot / 2, units = pairs + (P.D - P.rot);
-  const long long t = (long long)blockIdx.x * kRotThreads + threadIdx.x;
-  if (t >= (long long)P.B * P.N * units) return;
-  const int u = (int)(t % units);
-  const long long row = t / units;
-  const int n = (int)(row % P.N), b = (int)(row / P.N);
-  const bool turn = u < pairs;
-  int c0, c1 = 0;
-  float cs = 1.0f, sn = 0.0f;
-  if (turn) {
-    c0 = P.first + (P.interleaved ? 2 * u : u);
-    c1 = c0 + (P.interleaved ? 1 : pairs);
-    rotary_angle(P, rotary_position(P, b, n), u, cs, sn);
-  } else {
-    c0 = u - pairs;
-    if (c0 >= P.first) c0 += P.rot;
+  const int tid = threadIdx.x, pairs = P.rot / 2;
+  const long long row0 = (long long)blockIdx.x * kAnyRows;
+  const int rows = (int)min((long long)kAnyRows, (long long)P.B * P.N - row0);
+  const RotaryRows share(P);
+  for (int i = tid; i < 2 * rows; i += kRotThreads) {
+    const int s = i / rows, r = i - s * rows;
+    const RotaryTensor& X = P.t[s];
+    const long long b = (row0 + r) / P.N, n = row0 + r - b * P.N;
+    from[s * kAnyRows + r] = b * X.sb + n * X.sn;
+    to[s * kAnyRows + r] = (b * X.H * P.N + n) * D;
   }
-  const RotaryRows rows(P);
-  // (rows are loaded together before any is stored: in place, the compiler may not reorder them)
-#pragma unroll 1
-  for (int i0 = 0; i0 < rows.n; i0 += kPairAhead) {
-    T p[kPairAhead], q[kPairAhead];
-    T* y[kPairAhead];
+  for (int i = tid; i < rows * pairs; i += kRotThreads) {
+    const int r = i / pairs, c = i - r * pairs;
+    const long long b = (row0 + r) / P.N;
+    rotary_angle(P, rotary_position(P, (int)b, (int)(row0 + r - b * P.N)), c, turn[i].x, turn[i].y);
+  }
+  __syncthreads();
+  auto head = [&](int q) { return share.h0 + (q >= share.n0 ? q - share.n0 : q); };
+  float4 held[pieces];  // the next head's pieces
+  auto fetch = [&](int q) {
+    const int s = q >= share.n0;
+    const RotaryTensor& X = P.t[s];
+    const T* x = static_cast<const T*>(X.x) + head(q) * X.sh;
 #pragma unroll
-    for (int i = 0; i < kPairAhead; ++i)
-      if (i0 + i < rows.n) {
-        const T* x;
-        rows.at(P, b, n, i0 + i, x, y[i]);
-        p[i] = x[c0];
-        if (turn) q[i] = x[c1];
-      }
+    for (int k = 0; k < pieces; ++k) {
+      const int i = tid + k * kRotThreads, r = i / row_pieces, c = (i % row_pieces) * E;
+      if (r >= rows) break;
+      const T* src = x + from[s * kAnyRows + r] + c;
+      if (X.x_vec) {
+        held[k] = *reinterpret_cast<const float4*>(src);
+      } else {
+        T v[E];
 #pragma unroll
-    for (int i = 0; i < kPairAhead; ++i)
-      if (i0 + i < rows.n) {
-        if (turn) {
-          const float u = to_f32(p[i]), v = to_f32(q[i]);
-          y[i][c0] = from_f32<T>(u * cs - v * sn);
-          y[i][c1] = from_f32<T>(v * cs + u * sn);
-        } else {
-          y[i][c0] = p[i];
-        }
+        for (int e = 0; e < E; ++e) v[e] = src[e];
+        held[k] = *reinterpret_cast<const float4*>(v);
       }
+    }
+  };
+  if (share.n > 0) fetch(0);
+  for (int q = 0; q < share.n; ++q) {
+    const int s = q >= share.n0;
+    const RotaryTensor& X = P.t[s];
+#pragma unroll
+    for (int k = 0; k < pieces; ++k) {
+      const int i = tid + k * kRotThreads;
+      if (i / row_pieces < rows) reinterpret_cast<float4*>(tile)[i] = held[k];
+    }
+    if (q + 1 < share.n) fetch(q + 1);
+    __syncthreads();
+    int r = tid / pairs, c = tid - r * pairs;
+    const int dr = kRotThreads / pairs, dc = kRotThreads - dr * pairs;
+    for (int i = tid; i < rows * pairs; i += kRotThreads) {
+      T* u = tile + r * D + P.first + (P.interleaved ? 2 * c : c);
+      T* w = u + (P.interleaved ? 1 : pairs);
+      const float a = to_f32(*u), d = to_f32(*w);
+      const float2 t = turn[i];
+      *u = from_f32<T>(a * t.x - d * t.y);
+      *w = from_f32<T>(d * t.x + a * t.y);
+      r += dr;
+      c += dc;
+      if (c >= pairs) {
+        c -= pairs;
+        ++r;
+      }
+    }
+    __syncthreads();
+    T* y = static_cast<T*>(X.y) + (long long)head(q) * P.N * D;
+#pragma unroll
+    for (int k = 0; k < pieces; ++k) {
+      const int i = tid + k * kRotThreads, rr = i / row_pieces, cc = (i % row_pieces) * E;
+      if (rr >= rows) break;
+      T* dst = y + to[s * kAnyRows + rr] + cc;
+      const float4 v = reinterpret_cast<const float4*>(tile)[i];
+      if (X.y_vec) {
+        *reinterpret_cast<float4*>(dst) = v;
+      } else {
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int j = 0; j < E; ++j) dst[j] = e[j];
+      }
+    }
+    // (a thread writes the pieces that it then overwrites: no barrier until the next turn)
   }
 }
 
