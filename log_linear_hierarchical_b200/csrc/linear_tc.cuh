@@ -25,8 +25,18 @@
 // tokens reaches the chunk's other tokens, as through any tile of products.)
 //
 // Work split: a thread has one token row (a TMEM lane) and 32 of the D columns, so 8 warps at
-// D = 64, where two CTAs share an SM (112 KB of shared memory, 256 TMEM columns each), and 16 at
-// D = 128 (one CTA, 224 KB, 512 columns): 16 warps an SM either way.
+// D = 64, where two CTAs share an SM (113 KB of shared memory, 256 TMEM columns each), and 16 at
+// D = 128 (one CTA, 225 KB, 512 columns): 16 warps an SM either way.
+//
+// Measured at B = 1, H = 6, N = 65536 (47 segments of 11 chunks at D = 64, 24 of 22 at D = 128):
+// first pass 24 us (100 MB, 4.2 TB/s) and 44 us (201 MB, 4.5 TB/s), second pass 45 us (201 MB, 4.5
+// TB/s; 0.70 of the copy rate) and 83 us (403 MB, 4.9 TB/s); the three problems of a backward 124 and
+// 220 us.  No unit is saturated in the second pass (tensor cores 30 / 43 % active, shared memory 39 / 40 %
+// of its wavefronts from the warps and about as many again from the products' operands and the
+// copies, issue slots 42 / 39 %): it is bound by the latency of the chain S -> P -> O and W -> T ->
+// M -> O of a chunk, which the SM's other CTA (D = 64) or the other warps' phases (D = 128) cover in
+// part.  Fewer, busier warps made it slower every time.  Weighting Y into TMEM as the products' first operand
+// (no shared-memory writes) doubles the weighting at D = 64 and cost 20 us there.
 #pragma once
 
 #include "linear_common.cuh"
@@ -49,9 +59,9 @@ struct LtCfg {
   static constexpr int stage = (OUT ? 3 : 2) * tile;
   static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's second terms
   static constexpr int tab = mop + (OUT ? 1 : 2) * tile;
-  static constexpr int bars = tab + (132 + 32 + 64) * 4;
-  static constexpr int taddr = bars + 12 * 8;
-  static constexpr int smem = taddr + 16;
+  static constexpr int bars = tab + (132 + 64) * 4;
+  static constexpr int taddr = tab + 130 * 4;     // (pw leaves three of its places free)
+  static constexpr int smem = bars + 15 * 8;
   // TMEM columns.  P overlays the S columns of blocks 0 and 1 (both are in registers before
   // either is overwritten).  At D = 128 there are two O, so that a chunk's output leaves while the
   // next chunk's X M runs; at D = 64 the other CTA of the SM fills that time.  Without OUT there
@@ -61,7 +71,12 @@ struct LtCfg {
   static constexpr uint32_t cols = OUT ? (defer ? 512 : 256) : 2 * D;
 };
 
-enum : int { kLtFull = 0, kLtS = 2, kLtX, kLtY, kLtT, kLtP, kLtO, kLtM, kLtOut, kLtBars };
+// Barriers.  A wait is for a phase's parity, so nobody may fall two phases behind: a barrier's next
+// phase always needs something that every waiter does after its wait.  Where chunks overlap (the
+// first pass weights chunk c + 1 before it folds T of chunk c; the TMA warp runs beside both) that takes
+// two of them: kLtY and kLtT by the chunk's parity, kLtFull, kLtFree (a stage's products are done) and
+// kLtOut (its output is staged) by stage.
+enum : int { kLtS, kLtX, kLtP, kLtO, kLtM, kLtY, kLtT = 7, kLtOut = 9, kLtFree = 11, kLtFull = 13, kLtBars = 15 };
 
 struct alignas(64) LinearTcParams {
   CUtensorMap map[7];
@@ -214,8 +229,9 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   auto bar = [&](int i) { return bars + 8u * i; };
   // Powers of l, made once: an exponential in the loop costs 20 instructions a thread.
   float* pw = reinterpret_cast<float*>(base + Cfg::tab);  // pw[n] = l^n, 0 <= n <= 128
-  float* colf = pw + 132;                                 // weight of a block's column j at its edge
-  float* diag = colf + 32;  // diag[32 + column - row] = f1 l^distance in a block on the diagonal, 0 past it
+  // f1 l^distance for the blocks of P: diag[column - row] in a block on the diagonal (0 past it), and
+  // edge[column] from a block's column to its edge (the last column, or reversed the first).
+  float* near = pw + 132;  // 64 values
   uint32_t* taddr = reinterpret_cast<uint32_t*>(base + Cfg::taddr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const LinearParams& P = Q.P;
@@ -225,11 +241,14 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   const LinearProblem& R = P.p[prob];
   const int b = bh / P.H, h = bh % P.H;
   const bool rev = R.rev;
+  const float *diag = near + (rev ? 32 : 31), *edge = near + (rev ? 32 : 0);
 
   if (threadIdx.x == 0) {
     if (sb & 1023u) record_error(LLSA_ERR_INTERNAL);  // the swizzle needs 1024-byte alignment
-    for (int i = 0; i < kLtBars; ++i)
-      mbar_init(bar(i), i == kLtY || i == kLtP || i == kLtM || i == kLtOut ? Cfg::compute / 32 : 1);
+    for (int i = 0; i < kLtBars; ++i) {
+      const bool warps = i == kLtP || i == kLtM || i == kLtY || i == kLtY + 1 || i == kLtOut || i == kLtOut + 1;
+      mbar_init(bar(i), warps ? Cfg::compute / 32 : 1);
+    }
     mbar_fence_init();
   }
   if (warp == 4 * G + 1) {
@@ -242,9 +261,8 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   const float a = linear_decay(P.log_decay, h), a2 = a * kLog2e;
   if (threadIdx.x < 129) pw[threadIdx.x] = exp2f(a2 * (float)threadIdx.x);
   if (threadIdx.x >= 192 && threadIdx.x < 256) {
-    const int j = (int)threadIdx.x - 192, dist = rev ? j - 32 : 32 - j;
-    diag[j] = dist < 0 ? 0.0f : R.f1 * exp2f(a2 * (float)dist);
-    if (j < 32) colf[j] = exp2f(a2 * (float)(rev ? j : 31 - j));
+    const int k = (int)threadIdx.x - 192, dist = rev ? k - 32 : 31 - k;
+    near[k] = dist < 0 ? 0.0f : R.f1 * exp2f(a2 * (float)dist);
   }
   lt_fence_before();
   __syncthreads();
@@ -279,18 +297,16 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       }
       for (int c = 0; c < (OUT ? chunks : chunks - 2); ++c) {
         const bool more = c + 2 < chunks;
-        if (more) {  // Y is free once T is formed, Z once O is
-          ok = mbar_wait(bar(kLtT), c & 1);
+        if (more) {  // the chunk's products are done: Y and Z are free
+          ok = mbar_wait(bar(kLtFree + (c & 1)), c >> 1 & 1);
           if (!ok) break;
           expect(c + 2);
           ++loaded;
           load(c + 2, &Q.map[Q.iy[prob]], 0);
-          if (OUT) ok = mbar_wait(bar(kLtO), c & 1);
-          if (!ok) break;
           load(c + 2, &Q.map[Q.iz[prob]], 1);
         }
         if (OUT) {  // X's place holds the chunk's output
-          ok = mbar_wait(bar(kLtOut), c & 1);
+          ok = mbar_wait(bar(kLtOut + (c & 1)), c >> 1 & 1);
           if (!ok) break;
           const uint32_t src = sb + (c & 1) * Cfg::stage + 2 * Cfg::tile;
 #pragma unroll
@@ -318,10 +334,11 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
     for (int c = 0; c < chunks && ok; ++c) {
       const uint32_t y = sb + (c & 1) * Cfg::stage, z = y + Cfg::tile, x = y + 2 * Cfg::tile, m = sb + Cfg::mop;
       const uint32_t o = tmem + Cfg::col_o + (Cfg::defer ? (c & 1) * D : 0);
+      wait(kLtFull + (c & 1), c >> 1 & 1);
+      if (!ok) break;
       if (OUT) {
         // S needs the last chunk's P read (its O complete); O needs M
         const uint32_t dx = lt_desc(x, 16), dy = lt_desc(y, 16), dm = lt_desc(m, sub);
-        wait(kLtFull + (c & 1), (c >> 1) & 1);
         if (c > 0) wait(kLtO, (c - 1) & 1);
         if (!ok) break;
         lt_fence_after();
@@ -345,7 +362,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         last = kLtX, last_parity = c & 1;
       }
       if (wants_state(c)) {
-        wait(kLtY, c & 1);
+        wait(kLtY + (c & 1), c >> 1 & 1);
         if (!ok) break;
         lt_fence_after();
         const uint32_t y2 = OUT ? x : m + (c & 1) * Cfg::tile;
@@ -358,10 +375,11 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
 #pragma unroll
             for (int k = 0; k < C / 16; ++k) lt_mma(t, dy2 + mn_major(k), dz + mn_major(k), id_t, 1);
           }
-          lt_commit(bar(kLtT));
+          lt_commit(bar(kLtT + (c & 1)));
+          if (!OUT && c + 2 < chunks) lt_commit(bar(kLtFree + (c & 1)));
         }
         __syncwarp();
-        last = kLtT, last_parity = c & 1;
+        last = kLtT + (c & 1), last_parity = c >> 1 & 1;
       }
       if (OUT) {
         wait(kLtP, c & 1);
@@ -373,6 +391,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           for (int k = 0; k < C / 16; ++k)
             lt_mma_ts(o, tmem + Cfg::col_p + 8 * k, dz + mn_major(k), id_o, 1);
           lt_commit(bar(kLtO));
+          if (c + 2 < chunks) lt_commit(bar(kLtFree + (c & 1)));
         }
         __syncwarp();
         last = kLtO, last_parity = c & 1;
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       }
       fence_proxy_async();
       lt_fence_before();
-      lt_arrive(bar(kLtY));
+      lt_arrive(bar(kLtY + (c & 1)));
     };
     // M + M (l^n - 1) + T rather than l^n M + T: a factor close to 1 repeated over thousands of
     // chunks would add up its rounding
@@ -476,18 +495,18 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       uint32_t s[32];
       lt_ld32(tmem + lanes + Cfg::col_s + 32 * jb, s);
       if (past < 0) {
-        const float e1 = R.f1 * pw[rev ? 32 * jb - i : i - 32 * jb - 31];
+        const float e1 = pw[rev ? 32 * jb - i : i - 32 * jb - 31];
         const float2 e = make_float2(e1, e1);
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 w = *reinterpret_cast<const float4*>(colf + j);
+          const float4 w = *reinterpret_cast<const float4*>(edge + j);
           const float2 u = lt_mul2(lt_f2(s[j], s[j + 1]), lt_mul2(make_float2(w.x, w.y), e));
           const float2 v = lt_mul2(lt_f2(s[j + 2], s[j + 3]), lt_mul2(make_float2(w.z, w.w), e));
           s[j] = __float_as_uint(u.x), s[j + 1] = __float_as_uint(u.y);
           s[j + 2] = __float_as_uint(v.x), s[j + 3] = __float_as_uint(v.y);
         }
       } else {
-        const float* w = diag + 32 - lane;
+        const float* w = diag - lane;
 #pragma unroll
         for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * w[j]);
       }
@@ -512,7 +531,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         *reinterpret_cast<uint4*>(dst + swz(i, piece + e)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       fence_proxy_async();
       lt_fence_before();
-      lt_arrive(bar(kLtOut));
+      lt_arrive(bar(kLtOut + (c & 1)));
     };
     if (OUT) {
       store_m();
@@ -558,7 +577,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         lt_fence_before();
         lt_arrive(bar(kLtP));
         if (wants_state(c)) {
-          wait(kLtT, c & 1);
+          wait(kLtT + (c & 1), c >> 1 & 1);
           if (!ok) break;
           lt_fence_after();
           fold_t(c, n);
@@ -589,7 +608,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           weight_y(c, min(C, hi - chunk_at(c)));
         }
         if (c > 0) {
-          wait(kLtT, (c - 1) & 1);
+          wait(kLtT + ((c - 1) & 1), (c - 1) >> 1 & 1);
           if (!ok) break;
           lt_fence_after();
           fold_t(c - 1, min(C, hi - chunk_at(c - 1)));
