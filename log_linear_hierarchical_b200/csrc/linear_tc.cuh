@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       float* dst = R.state + (OUT ? (long long)bh : (long long)bh * P.nseg + seg) * (D * D) + sr * D + W * g;
       if (D == 64) {  // the two terms' halves meet in the copy's place, which no product reads now
         float2* other = reinterpret_cast<float2*>(base + Cfg::mop) + W / 2 * g * D + sr;  // [column pair][row]
+        lt_bar(5, Cfg::compute);  // (without a chunk nothing else orders the copy's writes before these)
         if (!first_term) {
 #pragma unroll
           for (int e = 0; e < W / 2; ++e) other[e * D] = m[e];

@@ -25,3 +25,19 @@ def test_repeats(D, B, H, N):
         else:
             assert all(torch.equal(x, y) for x, y in zip(got, first))
     assert llsa.llsa_device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,H,N", [(5, 2, 290), (100, 4, 200), (1, 2, 3000)])
+def test_empty_rows_keep_their_state(D, dtype, B, H, N):
+    q, k, v, do = (torch.full((B, H, N, D), float("nan"), device="cuda", dtype=dtype) for _ in range(4))
+    s0, ds = torch.randn(B, H, D, D, device="cuda"), torch.randn(B, H, D, D, device="cuda")
+    a = torch.full((H,), -0.1, device="cuda")
+    leaves = [t.requires_grad_() for t in (q, k, v, s0)]
+    lengths = torch.zeros(B, device="cuda", dtype=torch.int32)
+    for _ in range(20):
+        o, fin = llsa.llsa_linear_attention(q, k, v, a, initial_state=s0, lengths=lengths, return_state=True)
+        grads = torch.autograd.grad([o, fin], leaves, [do, ds])
+        assert torch.equal(fin, s0) and torch.equal(grads[3], ds)
+        assert not any(t.any() for t in (o, *grads[:3]))
