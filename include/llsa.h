@@ -469,7 +469,7 @@ typedef struct {
 
 llsa_status llsa_linear_validate(const llsa_linear_shape* shape);
 size_t llsa_linear_states_elems(const llsa_linear_shape* shape);    /* fp32 elements of states */
-size_t llsa_linear_workspace_bytes(const llsa_linear_shape* shape); /* of llsa_linear_backward */
+size_t llsa_linear_workspace_bytes(const llsa_linear_shape* shape); /* enough for llsa_linear_backward */
 
 llsa_status llsa_linear_forward(const llsa_linear_shape* shape, const void* q, const void* k, const void* v,
                                 const float* log_decay, const int32_t* lengths, const float* initial_state, void* o,

@@ -3,9 +3,12 @@
 // is one module global per device.
 #include <cudaTypedefs.h>
 
+#include <math.h>
+
 #include <atomic>
 #include <mutex>
 #include <new>
+#include <type_traits>
 
 #include "attn_simt.cuh"
 #include "linear_f32.cuh"
@@ -1007,24 +1010,50 @@ llsa_status linear_validate(const llsa_linear_shape* s) {
   return LLSA_OK;
 }
 
-// Segments of a sequence.  A cut costs a second read of two of the streams (the first pass),
-// so the sequence stays whole when the (batch, head) pairs alone fill half of the GPU's CTA
-// slots; otherwise there are as many segments as fill the slots, of whole 128-token chunks.
+// Segments of a sequence, for a pass of `problems` (1: forward, 3: backward) CTAs a segment.  Whole, every
+// (batch, head) is one chain of chunks; cut, there are as many segments as fill the CTA slots, for the
+// price of two more launches and of the first pass's work (half of a chunk's).  The estimate is in
+// microseconds, from measurements at 6 to 98 (batch, head) pairs of 256 to 4096 tokens, in which it picks the
+// faster form or one within 12 %, for example (whole against cut):
+//   D = 64:  6 x 512 11.3 / 12.5, 6 x 1024 20.3 / 12.7, 36 x 4096 73 / 36, 74 x 4096 74 / 58, 98 x 1024 21 / 29;
+//            backward 24 x 4096 77 / 53, 48 x 4096 78 / 86, 98 x 4096 111 / 152
+//   D = 128: 6 x 512 15.8 / 18.5, 24 x 4096 92 / 51, 74 x 4096 94 / 105;
+//            backward 12 x 4096 92 / 65, 24 x 4096 92 / 95, 74 x 4096 201 / 239
 struct LinearCut {
   int nseg, seg;
 };
-LinearCut linear_cut(const llsa_linear_shape* s) {
+
+// A chunk's time when `ctas` CTAs share the GPU: a chain of its own up to one CTA an SM (at D = 128 memory
+// slows it by then), beyond that the SMs' throughput.  128 tokens of fp32 take 6 (D = 64) and 10 times
+// as long.
+double linear_chunk_us(const llsa_linear_shape* s, double ctas) {
+  const double f = s->dtype == LLSA_BF16 ? 1 : s->D == 64 ? 6 : 10;
+  if (s->D == 64) return f * (ctas <= kSms ? 2.3 : fmax(2.3, 4.1 * ctas / (2 * kSms)));
+  if (ctas > kSms) return f * 3.9 * ctas / kSms;
+  return f * (2.8 + 0.8 * fmax(0.0, 2 * ctas / kSms - 1));
+}
+
+LinearCut linear_cut(const llsa_linear_shape* s, int problems) {
   const long long slots = kSms * (s->D == 64 ? 2 : 1), bh = (long long)s->B * s->H;
   const long long chunks = ((long long)s->N + 127) / 128;
-  long long n = 2 * bh > slots ? 1 : slots / bh;
+  long long n = bh > slots ? 1 : slots / bh;
   if (n > chunks) n = chunks;
-  const long long seg = (chunks + n - 1) / n;
-  n = (chunks + seg - 1) / seg;
-  return LinearCut{(int)n, (int)(seg * 128 < (1LL << 30) ? seg * 128 : (1LL << 30))};
+  const long long each = (chunks + n - 1) / n;
+  n = (chunks + each - 1) / each;
+  if (n > 1) {
+    const double whole = chunks * linear_chunk_us(s, (double)problems * bh);
+    const double cut = (s->D == 64 ? 10 : 17) + each * (0.5 * linear_chunk_us(s, (double)bh * n) +
+                                                        linear_chunk_us(s, (double)problems * bh * n));
+    if (whole <= cut) n = 1;
+  }
+  // the backward starts from the states that the forward left at its segments
+  if (problems > 1 && n > 1) return linear_cut(s, 1);
+  const long long seg = (n == 1 ? chunks : each) * 128;
+  return LinearCut{(int)n, (int)(seg < (1LL << 30) ? seg : (1LL << 30))};
 }
 
 size_t linear_states(const llsa_linear_shape* s) {
-  const LinearCut c = linear_cut(s);
+  const LinearCut c = linear_cut(s, 1);
   return c.nseg == 1 ? 0 : (size_t)s->B * s->H * c.nseg * s->D * s->D;
 }
 
@@ -1143,18 +1172,25 @@ llsa_status linear_segment_states(const llsa_linear_shape* s, const LinearParams
   A.p[0].state = states;
   llsa_status st = linear_pass<false>(s, A, cs);
   if (st != LLSA_OK) return st;
-  const int dd = s->D * s->D;
-  const long long ctas = (long long)s->B * s->H * (dd / kScanThreads);
-  return launch(kKLinearScan, cs, [&] {
-    launch_pdl(linear_scan_kernel, dim3((unsigned)ctas), dim3(kScanThreads), 0, cs, states, init, last, P.log_decay,
-               P.lengths, P.H, P.N, P.nseg, P.seg, dd, P.p[0].rev);
-  });
+  auto scan = [&](auto* one, int per) -> llsa_status {
+    using V = std::remove_pointer_t<decltype(one)>;
+    const int dd = s->D * s->D / per;
+    const long long ctas = (long long)s->B * s->H * (dd / kScanThreads);
+    return launch(kKLinearScan, cs, [&] {
+      launch_pdl(linear_scan_kernel<V>, dim3((unsigned)ctas), dim3(kScanThreads), 0, cs, reinterpret_cast<V*>(states),
+                 reinterpret_cast<const V*>(init), reinterpret_cast<V*>(last), P.log_decay, P.lengths, P.H, P.N, P.nseg,
+                 P.seg, dd, P.p[0].rev);
+    });
+  };
+  // a value a thread while that is at most 16 warps an SM, else four
+  if ((long long)s->B * s->H * s->D * s->D <= kSms * 512LL) return scan(static_cast<float*>(nullptr), 1);
+  return scan(static_cast<float4*>(nullptr), 4);
 }
 
-LinearParams linear_params(const llsa_linear_shape* s, const float* log_decay, const int32_t* lengths) {
-  const LinearCut c = linear_cut(s);
+LinearParams linear_params(const llsa_linear_shape* s, int problems, const float* log_decay, const int32_t* lengths) {
+  const LinearCut c = linear_cut(s, problems);
   LinearParams P{};
-  P.nprob = 1;
+  P.nprob = problems;
   P.H = s->H;
   P.N = s->N;
   P.nseg = c.nseg;
@@ -1495,7 +1531,7 @@ llsa_status llsa_linear_forward(const llsa_linear_shape* s, const void* q, const
   if (need) lap.output(states, need * sizeof(float));
   if (lap.any()) return LLSA_ERR_INVALID_ARG;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  LinearParams P = linear_params(s, log_decay, lengths);
+  LinearParams P = linear_params(s, 1, log_decay, lengths);
   LinearProblem& Q = P.p[0];
   Q.x = linear_stream(s, q, s->q_strides);
   Q.y = linear_stream(s, k, s->k_strides);
@@ -1543,14 +1579,14 @@ llsa_status llsa_linear_backward(const llsa_linear_shape* s, const void* q, cons
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const LinearStream sq = linear_stream(s, q, s->q_strides), sk = linear_stream(s, k, s->k_strides),
                      sv = linear_stream(s, v, s->v_strides), sd = linear_stream(s, dO, s->dO_strides);
-  float* back = need ? static_cast<float*>(workspace) : nullptr;  // the segments' G
-  LinearParams P = linear_params(s, log_decay, lengths);
-  P.nprob = 3;
+  LinearParams P = linear_params(s, 3, log_decay, lengths);
+  const bool cut = P.nseg > 1;
+  float* back = cut ? static_cast<float*>(workspace) : nullptr;  // the segments' G
   const float f = s->scale;
-  P.p[0] = LinearProblem{sk, sq, sd, dv, need ? back : d_final, need ? nullptr : d_initial, f, 1.0f, f, 1, 0};
-  P.p[1] = LinearProblem{sv, sd, sq, dk, need ? back : d_final, nullptr, f, 1.0f, f, 1, 1};
-  P.p[2] = LinearProblem{sd, sv, sk, dq, need ? states : initial_state, nullptr, f, f, 1.0f, 0, 1};
-  if (need) {
+  P.p[0] = LinearProblem{sk, sq, sd, dv, cut ? back : d_final, cut ? nullptr : d_initial, f, 1.0f, f, 1, 0};
+  P.p[1] = LinearProblem{sv, sd, sq, dk, cut ? back : d_final, nullptr, f, 1.0f, f, 1, 1};
+  P.p[2] = LinearProblem{sd, sv, sk, dq, cut ? states : initial_state, nullptr, f, f, 1.0f, 0, 1};
+  if (cut) {
     st = linear_segment_states(s, P, back, d_final, d_initial, cs);
     if (st != LLSA_OK) return st;
   }
