@@ -215,20 +215,38 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     if stream is not None:  # copies and a new o belong to the stream that uses them
         with torch.cuda.stream(_torch_stream(stream)):
             return llsa_linear_step(q, k, v, log_decay, pool, scale, slots, out_slots, out)
-    if q.dim() != 3 or q.dtype not in _DTYPES:
-        raise ValueError(f"q: {tuple(q.shape)} {q.dtype}, expected [B, H, D] of bfloat16 or float32")
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, log_decay, pool)):
+    size, dtype = q.shape, q.dtype
+    if len(size) != 3 or dtype not in _DTYPES:
+        raise ValueError(f"q: {tuple(size)} {dtype}, expected [B, H, D] of bfloat16 or float32")
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or log_decay.requires_grad
+                                    or pool.requires_grad):
         raise ValueError("llsa_linear_step has no gradients: call it under no_grad")
-    B, H, D = q.shape
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape != q.shape or t.dtype != q.dtype:
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} does not go with q {tuple(q.shape)} {q.dtype}")
-    if pool.dim() != 4 or tuple(pool.shape[1:]) != (H, D, D) or pool.dtype != torch.float32:
+    if k.shape != size or k.dtype != dtype or v.shape != size or v.dtype != dtype:
+        raise ValueError(f"k, v: {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype} do not go with q "
+                         f"{tuple(size)} {dtype}")
+    B, H, D = size
+    if pool.dim() != 4 or pool.shape[1:] != (H, D, D) or pool.dtype != torch.float32:
         raise ValueError(f"pool: {tuple(pool.shape)} {pool.dtype}, expected [P, {H}, {D}, {D}] of float32")
-    shape = make_linear_shape(B, H, 1, D, q.dtype, scale)
+    shape = _step_shape(B, H, D, _DTYPES[dtype], D ** -0.5 if scale is None else float(scale))
     q, k, v = _dense(q), _dense(k), _dense(v)
-    o = q.new_empty(q.shape) if out is None else out
-    args = [_address(q, "q"), _address(k, "k"), _address(v, "v"), _f32(log_decay, H, "log_decay"), _address(pool, "pool"),
-            pool.shape[0], _i32(slots, B, "slots"), _i32(out_slots, B, "out_slots"), _output(shape, o, "out")]
-    _check("llsa_linear_step", _lib.load().llsa_linear_step(ctypes.byref(shape), *args, _current_stream(q)))
+    _on_device(q, "q")
+    o = q.new_empty(size) if out is None else out
+    status = _lib.load().llsa_linear_step(
+        shape, _address(q, "q"), _address(k, "k"), _address(v, "v"), _f32(log_decay, H, "log_decay"),
+        _address(pool, "pool"), pool.shape[0], _i32(slots, B, "slots"), _i32(out_slots, B, "out_slots"),
+        o.data_ptr() if out is None else _step_output(q, out), _current_stream(q))
+    if status:
+        _check("llsa_linear_step", status)
     return o
+
+
+def _step_output(q: torch.Tensor, out: torch.Tensor) -> int:
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"out: {tuple(out.shape)} {out.dtype} is not q's {tuple(q.shape)} {q.dtype}")
+    return _address(out, "out")
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_shape(B: int, H: int, D: int, code: int, scale: float):
+    """The (constant) shape of a single-token call, by reference."""
+    return ctypes.byref(LLSALinearShape(B, H, 1, D, code, scale))

@@ -3,6 +3,7 @@ the frequency tables."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -84,6 +85,12 @@ def _heads(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
 _Strides = ctypes.c_int64 * 3
 
 
+@functools.lru_cache(maxsize=1024)
+def _shape(*fields):
+    """A (constant) llsa_rotary_shape, by reference."""
+    return ctypes.byref(LLSARotaryShape(*fields))
+
+
 def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse) -> list:
     """One launch over one or two tensors; ``outs`` None makes new contiguous ones."""
     x = xs[0]
@@ -112,11 +119,11 @@ def _rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse
         outs = [t.new_empty(t.shape) for t in xs]
     two = len(xs) == 2
     stream = _current_stream(x)
-    shape = LLSARotaryShape(B, H, xs[1].shape[1] if two else 0, N, D, _DTYPES[x.dtype], 2 * frequencies.numel(),
-                            first, flags, scale)
+    shape = _shape(B, H, xs[1].shape[1] if two else 0, N, D, _DTYPES[x.dtype], 2 * frequencies.numel(), int(first),
+                   flags, float(scale))
     strides = [None if t.is_contiguous() else _Strides(*t.stride()[:3]) for t in xs]
     _check("llsa_rotary", _lib.load().llsa_rotary(
-        ctypes.byref(shape), xs[0].data_ptr(), strides[0], xs[1].data_ptr() if two else None,
+        shape, xs[0].data_ptr(), strides[0], xs[1].data_ptr() if two else None,
         strides[1] if two else None, pos, pos_stride, frequencies.data_ptr(), outs[0].data_ptr(),
         outs[1].data_ptr() if two else None, stream))
     return outs
