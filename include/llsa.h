@@ -401,7 +401,7 @@ llsa_status llsa_index_transpose_noalloc(const llsa_shape* shape, const int32_t*
  * result is rounded once.
  *
  * x: [B, H, N, D] `dtype`, channels contiguous, with any strides of batch, head and token (in
- * elements; x_strides NULL: contiguous), so a [B, N, H, D] projection is read in place.  x2
+ * elements, 0 where the values are shared; x_strides NULL: contiguous), so a [B, N, H, D] projection is read in place.  x2
  * (NULL: one tensor) has its own head count H2 and strides.  y, y2: [B, H, N, D] and
  * [B, H2, N, D] contiguous; y may be x itself when x is contiguous (in place), otherwise no
  * output may overlap an input or the other output (LLSA_ERR_INVALID_ARG).  These four

@@ -901,8 +901,9 @@ bool extent_of(const void* p, int B, int H, int N, int D, const long long (&st)[
   return true;
 }
 
+// Batch, head and token strides; contiguous ones without `given`.
 void strides_or_contiguous(const int64_t* given, int H, int N, int D, long long (&st)[3]) {
-  const bool none = !given || (given[0] == 0 && given[1] == 0 && given[2] == 0);
+  const bool none = !given;
   st[0] = none ? (long long)H * N * D : (long long)given[0];
   st[1] = none ? (long long)N * D : (long long)given[1];
   st[2] = none ? (long long)D : (long long)given[2];
@@ -1057,9 +1058,15 @@ size_t linear_states(const llsa_linear_shape* s) {
   return c.nseg == 1 ? 0 : (size_t)s->B * s->H * c.nseg * s->D * s->D;
 }
 
+// (a linear shape's strides of three zeros stand for contiguous)
+void linear_strides(const llsa_linear_shape* s, const int64_t (&given)[3], long long (&st)[3]) {
+  const bool none = given[0] == 0 && given[1] == 0 && given[2] == 0;
+  strides_or_contiguous(none ? nullptr : given, s->H, s->N, s->D, st);
+}
+
 LinearStream linear_stream(const llsa_linear_shape* s, const void* p, const int64_t (&given)[3]) {
   long long st[3];
-  strides_or_contiguous(given, s->H, s->N, s->D, st);
+  linear_strides(s, given, st);
   return LinearStream{p, st[0], st[1], st[2]};
 }
 
@@ -1210,7 +1217,7 @@ struct Overlaps {
   bool bad = false;
   void input(const llsa_linear_shape* s, const void* p, const int64_t (&given)[3]) {
     long long st[3];
-    strides_or_contiguous(given, s->H, s->N, s->D, st);
+    linear_strides(s, given, st);
     bad = bad || !extent_of(p, s->B, s->H, s->N, s->D, st, dtype_bytes(s->dtype), &in[nin++]);
   }
   void input(const void* p, size_t bytes) {

@@ -60,6 +60,26 @@ def test_a_pool_past_32_bits():
     assert torch.equal(llsa.llsa_linear_step(q, k, v, a, small), o) and torch.equal(pool[-2:], small)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rot,first", [(64, 0), (22, 5)])
+def test_rows_that_share_their_values(dtype, rot, first):
+    """Expanded inputs and gradients: strides of 0 in some or all of the first three dimensions."""
+    f, _ = llsa.llsa_rotary_frequencies(rot, device="cuda")
+    one = torch.randn(64, device="cuda").to(dtype)
+    for x in (one.expand(2, 3, 40, 64), torch.randn(40, 64, device="cuda").to(dtype).expand(2, 3, 40, 64),
+              torch.randn(2, 1, 1, 64, device="cuda").to(dtype).expand(2, 3, 40, 64)):
+        want = llsa.llsa_rotary(x.contiguous(), None, None, f, first=first)
+        assert torch.equal(llsa.llsa_rotary(x, None, None, f, first=first), want)
+        leaf = torch.randn(2, 3, 40, 64, device="cuda").to(dtype).requires_grad_()
+        y = llsa.llsa_rotary(leaf, None, None, f, first=first)
+        (g,) = torch.autograd.grad(y, leaf, x, retain_graph=True)
+        assert torch.equal(g, torch.autograd.grad(y, leaf, x.contiguous())[0])
+    a = torch.tensor([-0.1, -0.01, 0.0], device="cuda")
+    q = torch.randn(2, 3, 40, 64, device="cuda").to(dtype)
+    k = one.expand(2, 3, 40, 64)
+    assert torch.equal(llsa.llsa_linear_attention(q, k, k, a), llsa.llsa_linear_attention(q, k.contiguous(), k.contiguous(), a))
+
+
 def inputs(seed, B, H, N, D, dtype):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return [torch.randn(B, H, N, D, device="cuda", generator=g).to(dtype) for _ in range(4)]
