@@ -1189,8 +1189,10 @@ llsa_status linear_segment_states(const llsa_linear_shape* s, const LinearParams
                  P.seg, dd, P.p[0].rev);
     });
   };
-  // a value a thread while that is at most 16 warps an SM, else four
-  if ((long long)s->B * s->H * s->D * s->D <= kSms * 512LL) return scan(static_cast<float*>(nullptr), 1);
+  // one value a thread or four: the forms cross between 98 and 197 thousand values (16384 tokens, one /
+  // four: 6 heads of 64 29.6 / 33.9 us for the whole forward, 6 of 128 52.3 / 54.5, 12 of 128 80.8 / 80.3, 48
+  // of 64 135.5 / 127.7)
+  if ((long long)s->B * s->H * s->D * s->D <= 131072) return scan(static_cast<float*>(nullptr), 1);
   return scan(static_cast<float4*>(nullptr), 4);
 }
 
