@@ -133,14 +133,17 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, frequencies, interleaved, first, scale):
         ctx.set_materialize_grads(False)
-        ctx.args = (positions, frequencies, interleaved, first, scale)
+        # torch refuses a backward after either is written again, and tensors of inference mode at all
+        ctx.save_for_backward(*(t.clone() if t is not None and t.is_inference() else t for t in (positions, frequencies)))
+        ctx.args = (interleaved, first, scale)
         outs = _rotate([q] if k is None else [q, k], None, positions, frequencies, interleaved, first, scale, False)
         return outs[0] if k is None else tuple(outs)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, *grads):
-        positions, frequencies, interleaved, first, scale = ctx.args
+        positions, frequencies = ctx.saved_tensors
+        interleaved, first, scale = ctx.args
         there = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
         back = [None, None]
         if there:

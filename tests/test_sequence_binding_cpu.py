@@ -1,0 +1,45 @@
+"""What the Python side of the sequence operators does before and around the kernels, on host
+tensors: the kernels' launch is replaced where a call has to get past it."""
+import pytest
+import torch
+
+from log_linear_hierarchical_b200 import rotary
+
+
+def fake_rotate(xs, outs, positions, frequencies, interleaved, first, scale, inverse):
+    """A pass that depends on the positions and frequencies of the moment."""
+    turn = (positions[:, None] * frequencies[0]).to(xs[0].dtype)
+    return [t * (scale - turn if inverse else scale + turn) for t in xs]
+
+
+@pytest.mark.parametrize("which", ["positions", "frequencies"])
+def test_rotary_gradient_sees_a_rewritten_buffer(monkeypatch, which):
+    monkeypatch.setattr(rotary, "_rotate", fake_rotate)
+    q, k = (torch.randn(1, 2, 8, 64, requires_grad=True) for _ in range(2))
+    held = dict(positions=torch.arange(8), frequencies=torch.ones(32, dtype=torch.float64))
+    y, z = rotary.llsa_rotary(q, k, held["positions"], held["frequencies"])
+    torch.autograd.grad([y, z], [q, k], [torch.ones_like(y)] * 2, retain_graph=True)
+    held[which].add_(1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad([y, z], [q, k], [torch.ones_like(y)] * 2)
+
+
+def test_rotary_gradient_without_positions(monkeypatch):
+    seen = []
+    monkeypatch.setattr(rotary, "_rotate", lambda xs, outs, *a: seen.append(a) or [t.clone() for t in xs])
+    q = torch.randn(1, 2, 8, 64, requires_grad=True)
+    f = torch.ones(32, dtype=torch.float64)
+    y = rotary.llsa_rotary(q, None, None, f, interleaved=True, first=2, scale=0.5)
+    torch.autograd.grad(y, q, torch.ones_like(y))
+    assert [(a[0], a[2:]) for a in seen] == [(None, (True, 2, 0.5, False)), (None, (True, 2, 0.5, True))]
+    assert all(torch.equal(a[1], f) for a in seen)
+
+
+def test_rotary_gradient_with_a_table_made_in_inference_mode(monkeypatch):
+    monkeypatch.setattr(rotary, "_rotate", fake_rotate)
+    with torch.inference_mode():
+        pos, f = torch.arange(8), torch.ones(32, dtype=torch.float64)
+    q = torch.randn(1, 2, 8, 64, requires_grad=True)
+    y = rotary.llsa_rotary(q, None, pos, f)
+    (g,) = torch.autograd.grad(y, q, torch.ones_like(y))
+    assert torch.equal(g, (1 - torch.arange(8.0))[:, None].expand(1, 2, 8, 64))
