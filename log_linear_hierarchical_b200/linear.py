@@ -10,7 +10,7 @@ import torch
 from . import _lib
 from ._lib import LLSALinearShape
 from .api import _DTYPES, LLSAError, _check, _stream
-from .rotary import _current_stream, _on_device, _torch_stream
+from .rotary import _current_stream, _no_tangents, _on_device, _torch_stream
 
 
 def make_linear_shape(B: int, H: int, N: int, D: int, dtype, scale: float | None = None) -> LLSALinearShape:
@@ -157,6 +157,7 @@ class _LinearAttention(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, d_final=None):
+        _no_tangents(do, d_final)
         q, k, v, log_decay, initial_state, lengths, states = ctx.saved_tensors
         if do is None and d_final is None:
             return (None,) * 8
@@ -178,7 +179,7 @@ def llsa_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     """Linear attention with a decay for each head over [B, H, N, D] CUDA tensors (D = 64 or 128,
     bf16 or fp32): with S = exp(log_decay[h]) S + k_t v_t^T after each token, o_t = scale * S^T q_t
     (``scale`` 1/sqrt(D) by default).  Cost is linear in N; gradients reach q, k, v and
-    ``initial_state``.
+    ``initial_state`` (forward-mode dual tensors are refused).
 
     ``log_decay``: [H] fp32, at most 0 in ordinary use; a constant (it gets no gradient).
     ``initial_state``: [B, H, D, D] fp32, the state before the first token (default 0).
@@ -191,6 +192,7 @@ def llsa_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     ties a leaf's gradient to the stream that the leaf was first used on).
     Views whose rows are whole 16-byte pieces (a [B, N, H, D] projection transposed) are read in
     place; others are copied first."""
+    _no_tangents(q, k, v, log_decay, initial_state)
     if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay gets no gradient: pass it detached")
     q, k, v = _laid_out(q), _laid_out(k), _laid_out(v)
@@ -215,6 +217,7 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     if stream is not None:  # copies and a new o belong to the stream that uses them
         with torch.cuda.stream(_torch_stream(stream)):
             return llsa_linear_step(q, k, v, log_decay, pool, scale, slots, out_slots, out)
+    _no_tangents(q, k, v, log_decay, pool)
     size, dtype = q.shape, q.dtype
     if len(size) != 3 or dtype not in _DTYPES:
         raise ValueError(f"q: {tuple(size)} {dtype}, expected [B, H, D] of bfloat16 or float32")

@@ -7,6 +7,7 @@ import functools
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._lib import LLSARotaryShape
@@ -69,6 +70,14 @@ def _current_stream(t: torch.Tensor) -> int:
 
 def _torch_stream(stream) -> torch.cuda.Stream:
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
+def _no_tangents(*tensors) -> None:
+    """Refuses forward-mode dual tensors: the kernels read the primal's address, and the tangent would
+    be lost without a word."""
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError("forward-mode gradients (dual tensors) are not supported")
 
 
 def _heads(t: torch.Tensor, name: str, like: torch.Tensor) -> torch.Tensor:
@@ -142,6 +151,7 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, *grads):
+        _no_tangents(*grads)
         positions, frequencies = ctx.saved_tensors
         interleaved, first, scale = ctx.args
         there = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
@@ -164,12 +174,13 @@ def llsa_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
     each pair of channels, radians per position (``llsa_rotary_frequencies``); the 2 * len channels
     from ``first`` on are turned, in the half layout (c with c + len) or ``interleaved`` (2c with
     2c + 1), and multiplied by ``scale``; the others are copied.  Gradients reach q and k by the
-    inverse rotation (under grad, on the current stream).  ``inplace`` (contiguous tensors, no
+    inverse rotation (under grad, on the current stream); forward-mode dual tensors are refused.  ``inplace`` (contiguous tensors, no
     gradients): q and k themselves are overwritten and returned."""
     if stream is not None:  # copies and new tensors belong to the stream that uses them
         with torch.cuda.stream(_torch_stream(stream)):
             return llsa_rotary(q, k, positions, frequencies, interleaved=interleaved, first=first, scale=scale,
                                inplace=inplace)
+    _no_tangents(q, k, frequencies)
     if frequencies.requires_grad and torch.is_grad_enabled():
         raise ValueError("frequencies get no gradient: pass them detached")
     if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):

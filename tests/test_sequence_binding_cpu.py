@@ -2,7 +2,9 @@
 tensors: the kernels' launch is replaced where a call has to get past it."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
+import log_linear_hierarchical_b200 as llsa
 from log_linear_hierarchical_b200 import rotary
 
 
@@ -43,3 +45,46 @@ def test_rotary_gradient_with_a_table_made_in_inference_mode(monkeypatch):
     y = rotary.llsa_rotary(q, None, pos, f)
     (g,) = torch.autograd.grad(y, q, torch.ones_like(y))
     assert torch.equal(g, (1 - torch.arange(8.0))[:, None].expand(1, 2, 8, 64))
+
+
+DUAL = "forward-mode"
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_rotary_refuses_a_tangent(which):
+    args = [torch.randn(1, 2, 8, 64), torch.randn(1, 2, 8, 64), torch.ones(32, dtype=torch.float64)]
+    with forward_ad.dual_level():
+        args[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        with pytest.raises(ValueError, match=DUAL):
+            llsa.llsa_rotary(args[0], args[1], None, args[2])
+
+
+@pytest.mark.parametrize("which", range(5))
+def test_linear_attention_and_step_refuse_a_tangent(which):
+    tokens, state = [torch.randn(1, 2, 8, 64) for _ in range(3)], torch.zeros(1, 2, 64, 64)
+    args = [*tokens, torch.zeros(2), state]
+    one = [t[:, :, 0] for t in tokens] + args[3:]
+    with forward_ad.dual_level():
+        for a in (args, one):
+            a[which] = forward_ad.make_dual(a[which], torch.ones_like(a[which]))
+        with pytest.raises(ValueError, match=DUAL):
+            llsa.llsa_linear_attention(*args[:4], initial_state=args[4])
+        with pytest.raises(ValueError, match=DUAL):
+            llsa.llsa_linear_step(*one)
+
+
+def test_a_dual_level_alone_refuses_nothing():
+    x = torch.randn(1, 2, 8, 64)
+    with forward_ad.dual_level():
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            llsa.llsa_linear_attention(x, x, x, torch.zeros(2))
+
+
+def test_rotary_gradient_refuses_a_tangent(monkeypatch):
+    monkeypatch.setattr(rotary, "_rotate", fake_rotate)
+    q = torch.randn(1, 2, 8, 64, requires_grad=True)
+    y = rotary.llsa_rotary(q, None, torch.arange(8), torch.ones(32, dtype=torch.float64))
+    with forward_ad.dual_level():
+        dy = forward_ad.make_dual(torch.ones_like(y), torch.ones_like(y))
+        with pytest.raises(ValueError, match=DUAL):
+            torch.autograd.grad(y, q, dy)
