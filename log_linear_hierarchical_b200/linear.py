@@ -107,18 +107,17 @@ def _states(shape) -> int:
 def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None, initial_state=None,
                         final_state=None, stream=None) -> None:
     sd = _states(shape)
-    stream = _current_stream(q) if stream is None else _stream(stream)
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
             _tokens(shape, v, "v", shape.v_strides), _f32(log_decay, shape.H, "log_decay"),
             _i32(lengths, shape.B, "lengths"), _f32(initial_state, sd, "initial_state"), _output(shape, o, "o"),
             _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states")]
+    stream = _current_stream(q) if stream is None else _stream(stream)  # (q is on the device by now)
     _check("llsa_linear_forward", _lib.load().llsa_linear_forward(ctypes.byref(shape), *args, stream))
 
 
 def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None, workspace=None, lengths=None,
                          initial_state=None, d_final=None, d_initial=None, stream=None) -> None:
     sd = _states(shape)
-    stream = _current_stream(q) if stream is None else _stream(stream)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
             _tokens(shape, v, "v", shape.v_strides), _tokens(shape, do, "do", shape.dO_strides),
@@ -127,6 +126,7 @@ def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None,
             _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states"), _output(shape, dq, "dq"),
             _output(shape, dk, "dk"), _output(shape, dv, "dv"), _f32(d_initial, sd, "d_initial"),
             None if workspace is None else _address(workspace, "workspace")]
+    stream = _current_stream(q) if stream is None else _stream(stream)
     _check("llsa_linear_backward", _lib.load().llsa_linear_backward(ctypes.byref(shape), *args, nbytes, stream))
 
 

@@ -88,3 +88,12 @@ def test_rotary_gradient_refuses_a_tangent(monkeypatch):
         dy = forward_ad.make_dual(torch.ones_like(y), torch.ones_like(y))
         with pytest.raises(ValueError, match=DUAL):
             torch.autograd.grad(y, q, dy)
+
+
+def test_raw_calls_refuse_host_tensors():
+    x, a = torch.zeros(1, 2, 8, 64), torch.zeros(2)
+    shape = llsa.make_linear_shape(1, 2, 8, 64, torch.float32)
+    for call in (lambda: llsa.llsa_linear_forward(shape, x, x, x, a, x.clone()),
+                 lambda: llsa.llsa_linear_backward(shape, x, x, x, x, a, x.clone(), x.clone(), x.clone())):
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()
