@@ -92,6 +92,14 @@ def _f32(t: torch.Tensor | None, need: int, name: str) -> int | None:
     return _address(t, name)
 
 
+def _decay(t: torch.Tensor, H: int) -> int:
+    """Address of log_decay: one value a head, shared by the batch (decays of another shape are other
+    operators, not longer tables)."""
+    if t.shape != (H,):
+        raise ValueError(f"log_decay: {tuple(t.shape)}, expected ({H},), one value a head")
+    return _f32(t, H, "log_decay")
+
+
 def _i32(t: torch.Tensor | None, need: int, name: str) -> int | None:
     if t is None:
         return None
@@ -107,8 +115,9 @@ def _states(shape) -> int:
 def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None, initial_state=None,
                         final_state=None, stream=None) -> None:
     sd = _states(shape)
+    a = _decay(log_decay, shape.H)
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
-            _tokens(shape, v, "v", shape.v_strides), _f32(log_decay, shape.H, "log_decay"),
+            _tokens(shape, v, "v", shape.v_strides), a,
             _i32(lengths, shape.B, "lengths"), _f32(initial_state, sd, "initial_state"), _output(shape, o, "o"),
             _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states")]
     stream = _current_stream(q) if stream is None else _stream(stream)  # (q is on the device by now)
@@ -119,9 +128,10 @@ def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None,
                          initial_state=None, d_final=None, d_initial=None, stream=None) -> None:
     sd = _states(shape)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    a = _decay(log_decay, shape.H)
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
             _tokens(shape, v, "v", shape.v_strides), _tokens(shape, do, "do", shape.dO_strides),
-            _f32(log_decay, shape.H, "log_decay"), _i32(lengths, shape.B, "lengths"),
+            a, _i32(lengths, shape.B, "lengths"),
             _f32(initial_state, sd, "initial_state"), _f32(d_final, sd, "d_final"),
             _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states"), _output(shape, dq, "dq"),
             _output(shape, dk, "dk"), _output(shape, dv, "dv"), _f32(d_initial, sd, "d_initial"),
@@ -137,7 +147,6 @@ def _forward(q, k, v, log_decay, scale, initial_state, lengths, want_state):
     st, n, _ = _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)
     if st != 0:
         raise LLSAError("llsa_linear_validate", st)
-    _on_device(q, "q")
     o = q.new_empty(q.shape)
     final = q.new_empty((shape.B, shape.H, shape.D, shape.D), dtype=torch.float32) if want_state else None
     states = q.new_empty(n, dtype=torch.float32) if n else None
@@ -231,11 +240,12 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     if pool.dim() != 4 or pool.shape[1:] != (H, D, D) or pool.dtype != torch.float32:
         raise ValueError(f"pool: {tuple(pool.shape)} {pool.dtype}, expected [P, {H}, {D}, {D}] of float32")
     shape = _step_shape(B, H, D, _DTYPES[dtype], D ** -0.5 if scale is None else float(scale))
+    a = _decay(log_decay, H)
     q, k, v = _dense(q), _dense(k), _dense(v)
     _on_device(q, "q")
     o = q.new_empty(size) if out is None else out
     status = _lib.load().llsa_linear_step(
-        shape, _address(q, "q"), _address(k, "k"), _address(v, "v"), _f32(log_decay, H, "log_decay"),
+        shape, _address(q, "q"), _address(k, "k"), _address(v, "v"), a,
         _address(pool, "pool"), pool.shape[0], _i32(slots, B, "slots"), _i32(out_slots, B, "out_slots"),
         o.data_ptr() if out is None else _step_output(q, out), _current_stream(q))
     if status:

@@ -97,3 +97,17 @@ def test_raw_calls_refuse_host_tensors():
                  lambda: llsa.llsa_linear_backward(shape, x, x, x, x, a, x.clone(), x.clone(), x.clone())):
         with pytest.raises(ValueError, match="CUDA tensors"):
             call()
+
+
+@pytest.mark.parametrize("shape", [(1,), (4,), (3, 2), (3, 2, 8), (2, 1), (1, 2), ()])
+def test_a_log_decay_of_another_shape_is_refused(shape):
+    """One value a head: a decay for each request or token is another operator."""
+    x, a = torch.zeros(3, 2, 8, 64), torch.zeros(shape)
+    spec = llsa.make_linear_shape(3, 2, 8, 64, torch.float32)
+    for call in (lambda: llsa.llsa_linear_attention(x, x, x, a),
+                 lambda: llsa.llsa_linear_attention(x.clone().requires_grad_(), x, x, a),
+                 lambda: llsa.llsa_linear_step(x[:, :, 0], x[:, :, 0], x[:, :, 0], a, torch.zeros(3, 2, 64, 64)),
+                 lambda: llsa.llsa_linear_forward(spec, x, x, x, a, x.clone()),
+                 lambda: llsa.llsa_linear_backward(spec, x, x, x, x, a, x.clone(), x.clone(), x.clone())):
+        with pytest.raises(ValueError, match="log_decay"):
+            call()
