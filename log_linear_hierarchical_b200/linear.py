@@ -84,10 +84,11 @@ def _address(t: torch.Tensor, name: str) -> int:
     return _on_device(t, name).data_ptr()
 
 
-def _f32(t: torch.Tensor | None, need: int, name: str) -> int | None:
+def _f32(t: torch.Tensor | None, need: int, name: str, scratch: bool = False) -> int | None:
+    """Address of ``need`` fp32 values (scratch may have more)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() < need:
+    if t.dtype != torch.float32 or t.numel() < need or (t.numel() > need and not scratch):
         raise ValueError(f"{name}: {t.numel()} elements of {t.dtype}, expected {need} of float32")
     return _address(t, name)
 
@@ -119,7 +120,7 @@ def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None,
     args = [_tokens(shape, q, "q", shape.q_strides), _tokens(shape, k, "k", shape.k_strides),
             _tokens(shape, v, "v", shape.v_strides), a,
             _i32(lengths, shape.B, "lengths"), _f32(initial_state, sd, "initial_state"), _output(shape, o, "o"),
-            _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states")]
+            _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states", True)]
     stream = _current_stream(q) if stream is None else _stream(stream)  # (q is on the device by now)
     _check("llsa_linear_forward", _lib.load().llsa_linear_forward(ctypes.byref(shape), *args, stream))
 
@@ -133,7 +134,7 @@ def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None,
             _tokens(shape, v, "v", shape.v_strides), _tokens(shape, do, "do", shape.dO_strides),
             a, _i32(lengths, shape.B, "lengths"),
             _f32(initial_state, sd, "initial_state"), _f32(d_final, sd, "d_final"),
-            _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states"), _output(shape, dq, "dq"),
+            _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states", True), _output(shape, dq, "dq"),
             _output(shape, dk, "dk"), _output(shape, dv, "dv"), _f32(d_initial, sd, "d_initial"),
             None if workspace is None else _address(workspace, "workspace")]
     stream = _current_stream(q) if stream is None else _stream(stream)

@@ -1,4 +1,4 @@
-"""What the sequence operators keep for their backward passes, on the GPU."""
+"""What the sequence operators keep for their backward passes and refuse at their raw calls, on the GPU."""
 import pytest
 import torch
 
@@ -18,3 +18,21 @@ def test_rotary_refuses_a_gradient_at_rewritten_positions(which):
     held[which].mul_(2)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         torch.autograd.grad(y, q, dy)
+
+
+def test_raw_calls_refuse_states_of_another_size():
+    B, H, N, D = 2, 2, 40, 64
+    q, k, v, do, o, dq, dk, dv = (torch.randn(B, H, N, D, device="cuda") for _ in range(8))
+    a = torch.tensor([-0.1, -0.01], device="cuda")
+    shape = llsa.make_linear_shape(B, H, N, D, torch.float32)
+    for n in (B - 1, B + 1):  # a pool of other states is not a batch's
+        pool = torch.zeros(n, H, D, D, device="cuda")
+        for name in ("initial_state", "final_state"):
+            with pytest.raises(ValueError, match=name):
+                llsa.llsa_linear_forward(shape, q, k, v, a, o, **{name: pool})
+        for name in ("initial_state", "d_final", "d_initial"):
+            with pytest.raises(ValueError, match=name):
+                llsa.llsa_linear_backward(shape, q, k, v, do, a, dq, dk, dv, **{name: pool})
+    roomy = torch.zeros(1000, device="cuda")  # scratch may be larger than needed
+    llsa.llsa_linear_forward(shape, q, k, v, a, o, states=roomy)
+    assert torch.equal(o, llsa.llsa_linear_attention(q, k, v, a)) and llsa.llsa_device_status() == 0
