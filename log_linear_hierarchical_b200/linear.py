@@ -6,6 +6,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import LLSALinearShape
@@ -109,6 +110,12 @@ def _i32(t: torch.Tensor | None, need: int, name: str) -> int | None:
     return _address(t, name)
 
 
+def _written(*tensors) -> None:
+    """Counts a write that torch does not see, through an address, as it counts its own in-place
+    operations: a backward that saved the tensor before refuses to run."""
+    increment_version([t for t in tensors if t is not None])
+
+
 def _states(shape) -> int:
     return shape.B * shape.H * shape.D * shape.D
 
@@ -123,6 +130,7 @@ def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None,
             _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states", True)]
     stream = _current_stream(q) if stream is None else _stream(stream)  # (q is on the device by now)
     _check("llsa_linear_forward", _lib.load().llsa_linear_forward(ctypes.byref(shape), *args, stream))
+    _written(o, final_state)
 
 
 def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None, workspace=None, lengths=None,
@@ -139,6 +147,7 @@ def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None,
             None if workspace is None else _address(workspace, "workspace")]
     stream = _current_stream(q) if stream is None else _stream(stream)
     _check("llsa_linear_backward", _lib.load().llsa_linear_backward(ctypes.byref(shape), *args, nbytes, stream))
+    _written(dq, dk, dv, d_initial)
 
 
 def _forward(q, k, v, log_decay, scale, initial_state, lengths, want_state):
@@ -232,7 +241,7 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     if len(size) != 3 or dtype not in _DTYPES:
         raise ValueError(f"q: {tuple(size)} {dtype}, expected [B, H, D] of bfloat16 or float32")
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or log_decay.requires_grad
-                                    or pool.requires_grad):
+                                    or pool.requires_grad or (out is not None and out.requires_grad)):
         raise ValueError("llsa_linear_step has no gradients: call it under no_grad")
     if k.shape != size or k.dtype != dtype or v.shape != size or v.dtype != dtype:
         raise ValueError(f"k, v: {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype} do not go with q "
@@ -251,6 +260,7 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
         o.data_ptr() if out is None else _step_output(q, out), _current_stream(q))
     if status:
         _check("llsa_linear_step", status)
+    _written(pool, out)
     return o
 
 

@@ -8,6 +8,7 @@ import math
 
 import torch
 from torch.autograd import forward_ad
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._lib import LLSARotaryShape
@@ -191,4 +192,6 @@ def llsa_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
     if inplace and not all(t.is_contiguous() for t in xs):
         raise ValueError("inplace needs contiguous tensors")
     outs = _rotate(xs, xs if inplace else None, positions, frequencies, interleaved, first, scale, False)
+    if inplace:  # torch sees no write through an address: a backward that saved q or k would not either
+        increment_version(xs)
     return outs[0] if k is None else tuple(outs)

@@ -36,3 +36,30 @@ def test_raw_calls_refuse_states_of_another_size():
     roomy = torch.zeros(1000, device="cuda")  # scratch may be larger than needed
     llsa.llsa_linear_forward(shape, q, k, v, a, o, states=roomy)
     assert torch.equal(o, llsa.llsa_linear_attention(q, k, v, a)) and llsa.llsa_device_status() == 0
+
+
+def test_tensors_written_in_place_count_as_written():
+    """An earlier operation that saved one of them refuses its backward, as with torch's own in-place
+    operations."""
+    B, H, N, D = 2, 2, 40, 64
+    q, k, v, do, o, dq, dk, dv = (torch.randn(B, H, N, D, device="cuda") for _ in range(8))
+    s0, fin, ds0 = (torch.randn(B, H, D, D, device="cuda") for _ in range(3))
+    a, f = torch.tensor([-0.1, -0.01], device="cuda"), llsa.llsa_rotary_frequencies(D, device="cuda")[0]
+    shape = llsa.make_linear_shape(B, H, N, D, torch.float32)
+    one, out = [t[:, :, 0].contiguous() for t in (q, k, v)], torch.empty(B, H, D, device="cuda")
+    for call, written in (
+            (lambda: llsa.llsa_rotary(q, k, None, f, inplace=True), (q, k)),
+            (lambda: llsa.llsa_linear_step(*one, a, s0), (s0,)),
+            (lambda: llsa.llsa_linear_step(*one, a, s0, out=out), (s0, out)),
+            (lambda: llsa.llsa_linear_forward(shape, q, k, v, a, o, None, None, s0, fin), (o, fin)),
+            (lambda: llsa.llsa_linear_backward(shape, q, k, v, do, a, dq, dk, dv, initial_state=s0, d_initial=ds0),
+             (dq, dk, dv, ds0))):
+        for t in written:
+            w = torch.ones_like(t, requires_grad=True)
+            y = w * t
+            call()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.sum().backward()
+    with torch.inference_mode():
+        pool = torch.randn(B, H, D, D, device="cuda")
+    llsa.llsa_linear_step(*one, a, pool)

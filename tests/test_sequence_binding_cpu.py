@@ -111,3 +111,28 @@ def test_a_log_decay_of_another_shape_is_refused(shape):
                  lambda: llsa.llsa_linear_backward(spec, x, x, x, x, a, x.clone(), x.clone(), x.clone())):
         with pytest.raises(ValueError, match="log_decay"):
             call()
+
+
+@pytest.mark.parametrize("which", range(2))
+def test_rotary_in_place_counts_as_a_write(monkeypatch, which):
+    def turn_in_place(xs, outs, *rest):
+        for t in outs:
+            t.data.mul_(2)  # as the kernel does, unseen by torch
+        return outs
+
+    monkeypatch.setattr(rotary, "_rotate", turn_in_place)
+    w, f = torch.ones(1, 2, 8, 64, requires_grad=True), torch.ones(32, dtype=torch.float64)
+    x = [torch.randn(1, 2, 8, 64) for _ in range(2)]
+    y = w * x[which]
+    rotary.llsa_rotary(x[0], x[1], None, f, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        free = torch.ones(1, 2, 8, 64)
+    assert rotary.llsa_rotary(free, None, None, f, inplace=True) is free  # (counts no versions)
+
+
+def test_step_refuses_an_output_that_requires_grad():
+    x = torch.zeros(1, 2, 64)
+    with pytest.raises(ValueError, match="no gradients"):
+        llsa.llsa_linear_step(x, x, x, torch.zeros(2), torch.zeros(1, 2, 64, 64), out=x.clone().requires_grad_())
