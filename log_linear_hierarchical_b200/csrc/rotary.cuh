@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(const RotaryPar
       if (X.x_vec) {
         held[k] = *reinterpret_cast<const float4*>(src);
       } else {
-        T v[E];
+        alignas(16) T v[E];  // read back as one float4
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = src[e];
         held[k] = *reinterpret_cast<const float4*>(v);
