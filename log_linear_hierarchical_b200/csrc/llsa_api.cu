@@ -956,6 +956,12 @@ llsa_status rotary_launch(const llsa_rotary_shape* s, const void* x, const int64
     vec = vec && x_vec && aligned16(out[i]);
     P.t[i] = RotaryTensor{in[i], out[i], st[0], st[1], st[2], heads[i], x_vec, aligned16(out[i])};
   }
+  Extent table[2] = {};  // frequencies, positions
+  const long long freq_st[3] = {0, 0, 1}, pos_st[3] = {position_stride, 0, 1};
+  extent_of(frequencies, 1, 1, s->rot / 2, 1, freq_st, sizeof(double), &table[0]);
+  if (positions) extent_of(positions, s->B, 1, s->N, 1, pos_st, pos_align, &table[1]);
+  for (int i = 0; i < P.tensors; ++i)
+    if (eout[i].overlaps(table[0]) || (positions && eout[i].overlaps(table[1]))) return LLSA_ERR_INVALID_ARG;
   if (P.tensors == 2 && (eout[0].overlaps(eout[1]) || ein[0].overlaps(eout[1]) || ein[1].overlaps(eout[0])))
     return LLSA_ERR_INVALID_ARG;
   P.B = s->B;
@@ -1214,7 +1220,7 @@ bool aligned_or_null(const void* p, uintptr_t a) { return reinterpret_cast<uintp
 
 // The bytes that a call reads and writes, to refuse outputs that overlap anything else.
 struct Overlaps {
-  Extent in[8], out[5];
+  Extent in[9], out[5];
   int nin = 0, nout = 0;
   bool bad = false;
   void input(const llsa_linear_shape* s, const void* p, const int64_t (&given)[3]) {
@@ -1534,6 +1540,8 @@ llsa_status llsa_linear_forward(const llsa_linear_shape* s, const void* q, const
   lap.input(s, q, s->q_strides);
   lap.input(s, k, s->k_strides);
   lap.input(s, v, s->v_strides);
+  lap.input(log_decay, s->H * sizeof(float));
+  lap.input(lengths, s->B * sizeof(int32_t));
   if (initial_state != final_state) lap.input(initial_state, linear_state_bytes(s));
   lap.output(o, linear_token_bytes(s));
   lap.output(final_state, linear_state_bytes(s));
@@ -1578,6 +1586,8 @@ llsa_status llsa_linear_backward(const llsa_linear_shape* s, const void* q, cons
   lap.input(s, k, s->k_strides);
   lap.input(s, v, s->v_strides);
   lap.input(s, dO, s->dO_strides);
+  lap.input(log_decay, s->H * sizeof(float));
+  lap.input(lengths, s->B * sizeof(int32_t));
   lap.input(initial_state, linear_state_bytes(s));
   lap.input(d_final, linear_state_bytes(s));
   if (need) lap.input(states, need * sizeof(float));
