@@ -3,11 +3,15 @@
 // tokens taken from the segment's end).
 //
 // Products run on the tensor cores with fp32 accuracy: each factor is split into two TF32 terms,
-// x = hi + lo (hi: x with its low 13 bits cleared; lo = x - hi exactly, of which TF32 keeps 11 bits), and
+// x = hi + lo (hi: x rounded to 11 bits; lo = x - hi exactly, of which TF32 keeps 11 bits), and
 // lo hi + hi lo + hi hi of 8 channels at a time are formed on the tensor cores, smallest first, and
 // added to the sums on the FP32 pipes: the tensor cores' own additions cut off instead of
-// rounding, which over a chunk's sums cost 1.3e-6 of the result instead of 2e-7.  mma.sync m16n8k8 does 509 multiply-adds a cycle and SM here, so three of them
-// 170, against 128 of the FP32 pipes, with a quarter of their shared-memory reads (on those pipes
+// rounding, which over a chunk's sums cost 1.3e-6 of the result instead of 2e-7.  hi is rounded for the
+// same reason: cut off, lo would always have x's sign and be twice as large, and what is lost of it
+// and with lo lo would add up (7.4e-7 of the result; it is 8 % faster: B = 1, H = 6, N = 65536 forward
+// 387 against 416 us at D = 64 and 1185 against 1280 at D = 128; the conversion instruction for
+// the addition and mask took 459 and 1416).  mma.sync m16n8k8 does 509 multiply-adds a cycle and SM here, so
+// three of them 170, against 128 of the FP32 pipes, with a quarter of their shared-memory reads (on those pipes
 // with 4 x 4 register tiles this kernel took 3 to 4 times as long).  The accumulators are summed
 // into the state, which lives in registers, in fp32 once a chunk.
 //
@@ -35,8 +39,10 @@ __device__ __forceinline__ int lf_swz(int row) { return ((row & 3) << 3) | (row 
 struct LfPair {
   uint32_t hi, lo;
 };
+// (From 2^128 (1 - 2^-12) on hi is infinite and the product NaN, as for an infinite x.  A NaN whose bits
+// the addition carries past the sign still has a NaN for lo.)
 __device__ __forceinline__ LfPair lf_split(float x) {
-  const uint32_t hi = __float_as_uint(x) & 0xffffe000u;
+  const uint32_t hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   return LfPair{hi, __float_as_uint(x - __uint_as_float(hi))};
 }
 
