@@ -59,3 +59,20 @@ def test_fp32_root_mean_square_error(D, N):
     got, want = run(q, k, v, do, torch.tensor([-0.02, -0.002], device="cuda"), D ** -0.5, s0, ds)
     for name, x, w in zip(("o", "final", "dq", "dk", "dv", "d_initial"), got, want):
         assert np.linalg.norm(num(x) - w) <= 2.0 ** -21 * np.linalg.norm(w), name
+
+
+@pytest.mark.parametrize("D,N", [(64, 1500), (128, 700)])
+def test_bf16_root_mean_square_error(D, N):
+    """A rounding to bf16 is off by a value uniform in half a step, at most 2^-8 of what is rounded: 2^-8 / sqrt(3)
+    of it in the mean square.  Over random inputs a result is a sum of terms of either sign, whose rounded factor
+    (the masked product, or the state's copy) makes the sum off by that share of its own mean square; the result's
+    own rounding comes on top: sqrt(2 / 3) 2^-8 together, for each head alone.  States get tokens in two bf16 terms,
+    2^-16 / sqrt(3)."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v, do = (torch.randn(1, 3, N, D, device="cuda", generator=g).bfloat16() for _ in range(4))
+    s0, ds = (torch.randn(1, 3, D, D, device="cuda", generator=g) for _ in range(2))
+    got, want = run(q, k, v, do, torch.tensor([0.0, -0.02, -0.7], device="cuda"), D ** -0.5, s0, ds)
+    for name, x, w in zip(("o", "final", "dq", "dk", "dv", "d_initial"), got, want):
+        bound = 2.0 ** -16 / 3 ** 0.5 if x.dtype == F32 else (2 / 3) ** 0.5 * 2.0 ** -8
+        for h in range(3):
+            assert np.linalg.norm(num(x)[:, h] - w[:, h]) <= bound * np.linalg.norm(w[:, h]), (name, h)
