@@ -397,8 +397,8 @@ llsa_status llsa_index_transpose_noalloc(const llsa_shape* shape, const int32_t*
  * (first + 2c, first + 2c + 1).  At position p, with t = p * frequencies[c] radians,
  *   y_a = scale (x_a cos t - x_b sin t),  y_b = scale (x_b cos t + x_a sin t);
  * the other channels are copied.  With LLSA_ROTARY_INVERSE t is negated: the gradient of the
- * call without it (the same scale).  Angles are formed in fp64, the rotation is fp32, and the
- * result is rounded once.
+ * call without it (the same scale).  Angles are formed and reduced to a turn with twice fp64's
+ * digits and then rounded to fp32, the rotation is fp32, and the result is rounded once.
  *
  * x: [B, H, N, D] `dtype`, channels contiguous, with any strides of batch, head and token (in
  * elements, 0 where the values are shared; x_strides NULL: contiguous), so a [B, N, H, D] projection is read in place.  x2
@@ -409,7 +409,8 @@ llsa_status llsa_index_transpose_noalloc(const llsa_shape* shape, const int32_t*
  * multiple of 8 and rot a multiple of 16, go through a kernel of 16-byte accesses.
  * positions: int64 (int32 with LLSA_ROTARY_POSITIONS_I32) device array; token n of batch row b
  * has position positions[b * position_stride + n] (position_stride 0: the rows share them).
- * NULL: position n.  Any value of magnitude below 2^53 is fine.
+ * NULL: position n.  Any value of magnitude below 2^53 whose angles stay below 2^53 radians keeps
+ * fp32's accuracy.
  * frequencies: [rot / 2] fp64 device array, radians per position.
  * Rules: B, H, N >= 1; D == 64 or 128; rot even, 2 <= rot; first >= 0, first + rot <= D;
  * B * max(H, H2) * N < 2^31.
@@ -455,9 +456,10 @@ llsa_status llsa_rotary(const llsa_rotary_shape* shape, const void* x, const int
  * Arithmetic: bf16 inputs use bf16 tensor-core products with fp32 accumulation (the masked
  * products and the state's copy that q meets are rounded to bf16, the tokens that enter the state
  * keep 16 bits); fp32 inputs use products of two TF32 terms a factor (a product's relative error
- * is about 2^-23, at most 2^-19; magnitudes from 2^128 (1 - 2^-12) on count as infinite) and fp32 sums; states are fp32.  The results do not depend on timing (no atomics).  Tokens are
- * taken in chunks of 128 (fp32: 64): a NaN or infinity at a token may reach every output of its
- * chunk, the earlier ones too.
+ * is about 2^-23, at most 2^-19; magnitudes from 2^128 (1 - 2^-12) on count as infinite) and fp32
+ * sums; states are fp32.  The results do not depend on timing (no atomics).  Tokens are taken in
+ * chunks of 128 (fp32: 64): a NaN or infinity at a token may reach every output of its chunk, the
+ * earlier ones too.
  * Rules: B, H, N >= 1; D == 64 or 128; B * H * N < 2^31; N <= 2^30; H <= 65535.
  */
 typedef struct {

@@ -6,9 +6,10 @@
 // (interleaved); the other channels are copied.  The gradient is the same map with -t.
 //
 // Angles: position * frequency reaches 2^20 radians and more, where fp32 keeps no digit of
-// the angle's place in its turn.  The product is formed in fp64 and reduced there to the
-// nearest whole turn; the rest (at most half a turn, rounded to fp32 relative to itself)
-// goes through sincospif.
+// the angle's place in its turn, and from about 2^30 on one rounding of the product to fp64 is as large
+// as fp32's own.  So the product keeps its rounding's remainder and 1 / (2 pi) has two fp64 terms; the
+// whole turns are taken off the large part exactly, and the rest (about half a turn at most, rounded to
+// fp32 relative to itself) goes through sincospif.
 //
 // HBM streaming: each element is read once and written once.  The angles of a (batch row,
 // token, 8 pairs) are computed once by one thread and used for its share of the heads of
@@ -43,9 +44,10 @@ struct RotaryParams {
 };
 
 __device__ __forceinline__ void rotary_angle(const RotaryParams& P, double pos, int c, float& cs, float& sn) {
-  constexpr double kInv2Pi = 0.15915494309189533577;
-  double turns = pos * __ldg(P.freq + c) * kInv2Pi;
-  turns -= rint(turns);
+  constexpr double kTurn = 0x1.45f306dc9c883p-3, kTurnLow = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+  const double f = __ldg(P.freq + c);
+  const double t = __dmul_rn(pos, f), t_low = fma(pos, f, -t);
+  const double turns = fma(t, kTurn, -rint(__dmul_rn(t, kTurn))) + fma(t, kTurnLow, t_low * kTurn);
   sincospif(2.0f * (float)turns, &sn, &cs);
   cs *= P.scale;
   sn *= P.inverse ? -P.scale : P.scale;
