@@ -151,8 +151,8 @@ def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None,
 
 
 def _forward(q, k, v, log_decay, scale, initial_state, lengths, want_state):
-    if q.dim() != 4 or q.dtype not in _DTYPES:
-        raise ValueError(f"q: {tuple(q.shape)} {q.dtype}, expected [B, H, N, D] of bfloat16 or float32")
+    if q.dtype not in _DTYPES:
+        raise ValueError(f"q: dtype {q.dtype}, expected bfloat16 or float32")
     shape = make_linear_shape(*q.shape, q.dtype, scale)
     st, n, _ = _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)
     if st != 0:
@@ -212,6 +212,8 @@ def llsa_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     Views whose rows are whole 16-byte pieces (a [B, N, H, D] projection transposed) are read in
     place; others are copied first."""
     _no_tangents(q, k, v, log_decay, initial_state)
+    if q.dim() != 4:
+        raise ValueError(f"q: {tuple(q.shape)}, expected [B, H, N, D]")
     if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay gets no gradient: pass it detached")
     q, k, v = _laid_out(q), _laid_out(k), _laid_out(v)

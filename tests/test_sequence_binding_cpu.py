@@ -136,3 +136,11 @@ def test_step_refuses_an_output_that_requires_grad():
     x = torch.zeros(1, 2, 64)
     with pytest.raises(ValueError, match="no gradients"):
         llsa.llsa_linear_step(x, x, x, torch.zeros(2), torch.zeros(1, 2, 64, 64), out=x.clone().requires_grad_())
+
+
+def test_a_q_of_another_rank_is_refused_beside_a_state():
+    x, a, s0 = torch.zeros(1, 2, 8, 64), torch.zeros(2), torch.zeros(1, 2, 64, 64)
+    for q in (x[0], x[0, 0], x[None]):
+        for state in (None, s0):
+            with pytest.raises(ValueError, match="expected .B, H, N, D"):
+                llsa.llsa_linear_attention(q, x, x, a, initial_state=state)
