@@ -18,7 +18,12 @@ def make_linear_shape(B: int, H: int, N: int, D: int, dtype, scale: float | None
     """``scale``: the factor of every output, 1 / sqrt(D) by default.  The strides of q, k, v and
     dO are filled in by the calls that take the tensors."""
     code = _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return LLSALinearShape(B, H, N, D, code, D ** -0.5 if scale is None else float(scale))
+    return LLSALinearShape(B, H, N, D, code, _scale(D, scale))
+
+
+def _scale(D: int, scale: float | None) -> float:
+    """(a D that is refused later has no root)"""
+    return (D ** -0.5 if D > 0 else 1.0) if scale is None else float(scale)
 
 
 def llsa_linear_validate(shape: LLSALinearShape) -> int:
@@ -251,7 +256,7 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     B, H, D = size
     if pool.dim() != 4 or pool.shape[1:] != (H, D, D) or pool.dtype != torch.float32:
         raise ValueError(f"pool: {tuple(pool.shape)} {pool.dtype}, expected [P, {H}, {D}, {D}] of float32")
-    shape = _step_shape(B, H, D, _DTYPES[dtype], D ** -0.5 if scale is None else float(scale))
+    shape = _step_shape(B, H, D, _DTYPES[dtype], _scale(D, scale))
     a = _decay(log_decay, H)
     q, k, v = _dense(q), _dense(k), _dense(v)
     _on_device(q, "q")

@@ -144,3 +144,13 @@ def test_a_q_of_another_rank_is_refused_beside_a_state():
         for state in (None, s0):
             with pytest.raises(ValueError, match="expected .B, H, N, D"):
                 llsa.llsa_linear_attention(q, x, x, a, initial_state=state)
+
+
+def test_no_channels_are_refused_as_any_other_head_width():
+    assert llsa.llsa_linear_validate(llsa.make_linear_shape(1, 2, 8, 0, torch.float32)) == 1
+    assert llsa.llsa_linear_validate(llsa.make_linear_shape(1, 2, 8, -64, torch.float32)) == 1
+    x = torch.zeros(1, 2, 8, 0)
+    with pytest.raises(llsa.LLSAError):
+        llsa.llsa_linear_attention(x, x, x, torch.zeros(2))
+    with pytest.raises(ValueError):  # (host tensors; a ZeroDivisionError is none)
+        llsa.llsa_linear_step(x[:, :, 0], x[:, :, 0], x[:, :, 0], torch.zeros(2), torch.zeros(1, 2, 0, 0))
