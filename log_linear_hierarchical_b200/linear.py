@@ -188,7 +188,7 @@ class _LinearAttention(torch.autograd.Function):
         shape = make_linear_shape(*q.shape, q.dtype, ctx.scale)
         do = q.new_zeros(q.shape) if do is None else _laid_out(do)
         d_final = None if d_final is None else _dense(d_final)
-        dq, dk, dv = q.new_empty((3, *q.shape)).unbind(0)
+        dq, dk, dv = (q.new_empty(q.shape) for _ in range(3))  # (a kept gradient holds no other's memory or version)
         d_initial = torch.empty_like(initial_state) if ctx.needs_input_grad[5] else None
         n = _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[2]
         workspace = q.new_empty(n // 4, dtype=torch.float32) if n else None

@@ -63,3 +63,15 @@ def test_tensors_written_in_place_count_as_written():
     with torch.inference_mode():
         pool = torch.randn(B, H, D, D, device="cuda")
     llsa.llsa_linear_step(*one, a, pool)
+
+
+def test_gradients_own_their_memory():
+    """A gradient that is kept holds no other's memory, and writing one is no write of another."""
+    leaves = [torch.randn(1, 2, 200, 64, device="cuda", requires_grad=True) for _ in range(3)]
+    o = llsa.llsa_linear_attention(*leaves, torch.tensor([-0.1, -0.01], device="cuda"))
+    grads = torch.autograd.grad(o, leaves, torch.randn_like(o))
+    for g in grads:
+        assert g.untyped_storage().nbytes() == g.numel() * g.element_size() and not g._is_view()
+    before = [g._version for g in grads]
+    grads[0].mul_(2)
+    assert [g._version for g in grads[1:]] == before[1:]
