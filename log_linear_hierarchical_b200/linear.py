@@ -115,16 +115,12 @@ def _i32(t: torch.Tensor | None, need: int, name: str) -> int | None:
     return _address(t, name)
 
 
-def _written(*tensors) -> None:
-    """Counts a write that torch does not see, through an address, as it counts its own in-place
-    operations: a backward that saved the tensor before refuses to run."""
-    increment_version([t for t in tensors if t is not None])
-
-
 def _states(shape) -> int:
     return shape.B * shape.H * shape.D * shape.D
 
 
+# Writes through an address, which torch does not see, are counted with increment_version as torch counts its
+# own in-place operations: a backward that saved such a tensor before refuses to run.
 def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None, initial_state=None,
                         final_state=None, stream=None) -> None:
     sd = _states(shape)
@@ -135,7 +131,7 @@ def llsa_linear_forward(shape, q, k, v, log_decay, o, states=None, lengths=None,
             _f32(final_state, sd, "final_state"), _f32(states, _sizes(shape.B, shape.H, shape.N, shape.D, shape.dtype)[1], "states", True)]
     stream = _current_stream(q) if stream is None else _stream(stream)  # (q is on the device by now)
     _check("llsa_linear_forward", _lib.load().llsa_linear_forward(ctypes.byref(shape), *args, stream))
-    _written(o, final_state)
+    increment_version(o if final_state is None else (o, final_state))
 
 
 def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None, workspace=None, lengths=None,
@@ -152,7 +148,7 @@ def llsa_linear_backward(shape, q, k, v, do, log_decay, dq, dk, dv, states=None,
             None if workspace is None else _address(workspace, "workspace")]
     stream = _current_stream(q) if stream is None else _stream(stream)
     _check("llsa_linear_backward", _lib.load().llsa_linear_backward(ctypes.byref(shape), *args, nbytes, stream))
-    _written(dq, dk, dv, d_initial)
+    increment_version((dq, dk, dv) if d_initial is None else (dq, dk, dv, d_initial))
 
 
 def _forward(q, k, v, log_decay, scale, initial_state, lengths, want_state):
@@ -267,7 +263,7 @@ def llsa_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
         o.data_ptr() if out is None else _step_output(q, out), _current_stream(q))
     if status:
         _check("llsa_linear_step", status)
-    _written(pool, out)
+    increment_version(pool if out is None else (pool, out))
     return o
 
 

@@ -144,7 +144,11 @@ class _Rotary(torch.autograd.Function):
     def forward(ctx, q, k, positions, frequencies, interleaved, first, scale):
         ctx.set_materialize_grads(False)
         # torch refuses a backward after either is written again, and tensors of inference mode at all
-        ctx.save_for_backward(*(t.clone() if t is not None and t.is_inference() else t for t in (positions, frequencies)))
+        if frequencies.is_inference():
+            frequencies = frequencies.clone()
+        if positions is not None and positions.is_inference():
+            positions = positions.clone()
+        ctx.save_for_backward(positions, frequencies)
         ctx.args = (interleaved, first, scale)
         outs = _rotate([q] if k is None else [q, k], None, positions, frequencies, interleaved, first, scale, False)
         return outs[0] if k is None else tuple(outs)
