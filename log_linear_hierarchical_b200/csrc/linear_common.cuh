@@ -32,7 +32,7 @@ struct LinearProblem {
   LinearStream x, y, z;
   void* out;          // [B, H, N, D] contiguous; rows at or past the length are written 0
   const float* init;  // M at the start: per segment [BH][nseg][D][D] (per_segment) or [BH][D][D]; null: 0
-  float* state;       // M at the end, [BH][nseg][D][D] (per_segment_state) or [BH][D][D]; null: not wanted
+  float* state;       // M at the end, [BH][nseg][D][D] in the first pass over segments, else [BH][D][D]; null: not wanted
   float f1, f2, w;
   int rev;            // reversed time order
   int transpose;      // init holds M^T

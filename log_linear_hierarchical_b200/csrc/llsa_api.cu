@@ -1026,6 +1026,8 @@ llsa_status linear_validate(const llsa_linear_shape* s) {
 //            backward 24 x 4096 77 / 53, 48 x 4096 78 / 86, 98 x 4096 111 / 152
 //   D = 128: 6 x 512 15.8 / 18.5, 24 x 4096 92 / 51, 74 x 4096 94 / 105;
 //            backward 12 x 4096 92 / 65, 24 x 4096 92 / 95, 74 x 4096 201 / 239
+// Nothing was measured between 98 pairs and the CTA slots, where whole waves of CTAs differ from the
+// estimate's share of them, and above the slots a sequence is never cut.
 struct LinearCut {
   int nseg, seg;
 };

@@ -179,8 +179,11 @@ def llsa_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor
     each pair of channels, radians per position (``llsa_rotary_frequencies``); the 2 * len channels
     from ``first`` on are turned, in the half layout (c with c + len) or ``interleaved`` (2c with
     2c + 1), and multiplied by ``scale``; the others are copied.  Gradients reach q and k by the
-    inverse rotation (under grad, on the current stream); forward-mode dual tensors are refused.  ``inplace`` (contiguous tensors, no
-    gradients): q and k themselves are overwritten and returned."""
+    inverse rotation (under grad, on the current stream); forward-mode dual tensors are refused, and
+    so is a backward pass after ``positions`` or ``frequencies`` were written again.  Before a backward pass is
+    captured into a CUDA graph, drop eager graphs of the same leaves (torch ties a leaf's gradient to the
+    stream that the leaf was first used on).  ``inplace`` (contiguous tensors, no gradients): q and k
+    themselves are overwritten and returned."""
     if stream is not None:  # copies and new tensors belong to the stream that uses them
         with torch.cuda.stream(_torch_stream(stream)):
             return llsa_rotary(q, k, positions, frequencies, interleaved=interleaved, first=first, scale=scale,
