@@ -454,8 +454,9 @@ llsa_status llsa_rotary(const llsa_rotary_shape* shape, const void* x, const int
  * is 0) that llsa_linear_forward fills and llsa_linear_backward reads: the states at which the
  * segments that the sequence is cut into start.
  * Arithmetic: bf16 inputs use bf16 tensor-core products with fp32 accumulation (the masked
- * products and the state's copy that q meets are rounded to bf16, the tokens that enter the state
- * keep 16 bits); fp32 inputs use products of two TF32 terms a factor (a product's relative error
+ * products and the state's copy that q meets are rounded to bf16; the tokens that enter the state
+ * keep 24 bits for a final_state or d_initial that is asked for, 16 where only such roundings follow,
+ * so the last bits of o and dv may depend on that); fp32 inputs use products of two TF32 terms a factor (a product's relative error
  * is about 2^-23, at most 2^-19; magnitudes from 2^128 (1 - 2^-12) on count as infinite) and fp32
  * sums; states are fp32.  The results do not depend on timing (no atomics).  Tokens are taken in
  * chunks of 128 (fp32: 64): a NaN or infinity at a token may reach every output of its chunk, the

@@ -36,6 +36,7 @@ struct LinearProblem {
   float f1, f2, w;
   int rev;            // reversed time order
   int transpose;      // init holds M^T
+  int exact;          // the caller gets the state (or one made from it) as fp32
 };
 
 struct LinearParams {

@@ -5,6 +5,8 @@
 //   1. S = X Y^T and O = X M (M as bf16 in shared memory)                      (fp32, TMEM)
 //   2. Y <- w l^{n-1-j} Y, as two bf16 terms (the value and its rounding's remainder; the
 //      second takes X's place), then T = Y^T Z                                 (fp32, TMEM)
+//      (three terms when the caller gets the state: the third in X's place, the second in that
+//      of M's copy, which X M has read by then)
 //   3. O <- f2 l^{i+1} O;  P = f1 l^{i-j} S where j <= i, else 0, as bf16 into TMEM, then
 //      O += P Z while T is folded into M = l^n M + T (fp32 registers)
 //   4. O goes out as bf16 through X's place and a TMA store.
@@ -13,10 +15,14 @@
 //
 // Roundings to bf16: P and the copy of M that X multiplies, which are tensor-core operands (2^-8
 // of a term each, like the output's own rounding); the weighted Y would be a third, in the state
-// itself, which is why it is split (2^-16).  At D = 64 the two terms are the halves of one M = 128
-// product (M = 64 runs at half rate): lanes 0..63 hold the state's rows from the values, lanes
-// 64..127 those from the remainders, both decay alike, X meets them as one 128-row operand, and
-// they are added when the state leaves the kernel.  At D = 128 they are two products into one T.
+// itself, which is why it is split.  2^-16 is all that outputs can show, behind the rounding of M's
+// copy; a state that is returned is fp32, so its tokens have three terms, 2^-24 (2.5e-6 -> 1.3e-7 of
+// the state, for 5 to 20 % of the time: B = 8, H = 16, N = 1999, D = 128 71 -> 82 us, B = 32, H = 24,
+// N = 2048, D = 64 175 -> 207 us).  At D = 64 two terms are the halves of one M = 128 product (M = 64 runs
+// at half rate): lanes 0..63 hold the state's rows from the values, lanes 64..127 those from the
+// remainders, both decay alike, X meets them as one 128-row operand, and they are added when the
+// state leaves the kernel; with three terms a product of the third and half of the second precedes that
+// of the first and half of the second.  At D = 128 they are products into one T.
 //
 // Weights: l^{i-j} over a 32-column block of P is (l^{i - last column}) (l^{last column - j}), two
 // factors of at most 1, so one exponential a row and block serves 32 products and nothing
@@ -55,13 +61,14 @@ struct LtCfg {
   static constexpr int ctas_per_sm = D == 64 ? 2 : 1;
   static constexpr int sub = kLtChunk * 128;      // bytes of a sub-tile
   static constexpr int tile = subs * sub;
-  // a stage is Y, Z (and X); without OUT two more tiles hold Y's second terms
+  // a stage is Y, Z (and X); without OUT three more tiles hold Y's third terms and, by the chunk's
+  // parity, its second ones
   static constexpr int stage = (OUT ? 3 : 2) * tile;
-  static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's second terms
-  static constexpr int tab = mop + (OUT ? 1 : 2) * tile;
+  static constexpr int mop = 2 * stage;           // [128][D] bf16: M (OUT), or Y's third terms
+  static constexpr int tab = mop + (OUT ? 1 : 3) * tile;
   static constexpr int bars = tab + (132 + 64) * 4;
   static constexpr int taddr = tab + 130 * 4;     // (pw leaves three of its places free)
-  static constexpr int smem = bars + 15 * 8;
+  static constexpr int smem = bars + 16 * 8;
   // TMEM columns.  P overlays the S columns of blocks 0 and 1 (both are in registers before
   // either is overwritten).  At D = 128 there are two O, so that a chunk's output leaves while the
   // next chunk's X M runs; at D = 64 the other CTA of the SM fills that time.  Without OUT there
@@ -75,8 +82,11 @@ struct LtCfg {
 // phase always needs something that every waiter does after its wait.  Where chunks overlap (the
 // first pass weights chunk c + 1 before it folds T of chunk c; the TMA warp runs beside both) that takes
 // two of them: kLtY and kLtT by the chunk's parity, kLtFull, kLtFree (a stage's products are done) and
-// kLtOut (its output is staged) by stage.
-enum : int { kLtS, kLtX, kLtP, kLtO, kLtM, kLtY, kLtT = 7, kLtOut = 9, kLtFree = 11, kLtFull = 13, kLtBars = 15 };
+// kLtOut (its output is staged) by stage.  kLtThird (the first pass's third terms are read) needs one: its
+// next phase needs every warp's weights, which each applies after its wait.
+enum : int {
+  kLtS, kLtX, kLtP, kLtO, kLtM, kLtY, kLtT = 7, kLtOut = 9, kLtFree = 11, kLtFull = 13, kLtThird = 15, kLtBars = 16
+};
 
 struct alignas(64) LinearTcParams {
   CUtensorMap map[7];
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
   const int seg = (blockIdx.x / P.nprob) % P.nseg, bh = blockIdx.x / P.nprob / P.nseg;
   const LinearProblem& R = P.p[prob];
   const int b = bh / P.H, h = bh % P.H;
-  const bool rev = R.rev;
+  const bool rev = R.rev, exact = R.exact;
   const float *diag = near + (rev ? 32 : 31), *edge = near + (rev ? 32 : 0);
 
   if (threadIdx.x == 0) {
@@ -365,13 +375,23 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
         wait(kLtY + (c & 1), c >> 1 & 1);
         if (!ok) break;
         lt_fence_after();
-        const uint32_t y2 = OUT ? x : m + (c & 1) * Cfg::tile;
+        const uint32_t y2 = OUT ? (exact ? m : x) : m + (1 + (c & 1)) * Cfg::tile, y3 = OUT ? x : m;
         const uint32_t t = tmem + Cfg::col_t + (OUT ? 0 : (c & 1) * D);
         if (lt_elect()) {
           const uint32_t dy = lt_desc(y, D == 64 ? y2 - y : sub), dy2 = lt_desc(y2, sub), dz = lt_desc(z, sub);
+          if (exact) {  // smallest first: the third terms (D = 64: over the halves of the second ones)
+            const uint32_t dy3 = lt_desc(y3, D == 64 ? y2 - y3 : sub);
 #pragma unroll
-          for (int k = 0; k < C / 16; ++k) lt_mma(t, dy + mn_major(k), dz + mn_major(k), id_t, k > 0);
-          if (D == 128) {
+            for (int k = 0; k < C / 16; ++k) lt_mma(t, dy3 + mn_major(k), dz + mn_major(k), id_t, k > 0);
+            if (!OUT) lt_commit(bar(kLtThird));
+            if (D == 128) {
+#pragma unroll
+              for (int k = 0; k < C / 16; ++k) lt_mma(t, dy2 + mn_major(k), dz + mn_major(k), id_t, 1);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < C / 16; ++k) lt_mma(t, dy + mn_major(k), dz + mn_major(k), id_t, exact || k > 0);
+          if (D == 128 && !exact) {
 #pragma unroll
             for (int k = 0; k < C / 16; ++k) lt_mma(t, dy2 + mn_major(k), dz + mn_major(k), id_t, 1);
           }
@@ -437,17 +457,20 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
             make_uint4(pack_bf16(m[4 * e].x, m[4 * e].y), pack_bf16(m[4 * e + 1].x, m[4 * e + 1].y),
                        pack_bf16(m[4 * e + 2].x, m[4 * e + 2].y), pack_bf16(m[4 * e + 3].x, m[4 * e + 3].y));
     };
-    // Y's rows weighted, in place and in the second terms' tile; rows behind the last token are
+    // Y's rows weighted, in place and in the other terms' tiles; rows behind the last token are
     // zeroed (with Z's: their contents must not meet a product's zeros)
     auto weight_y = [&](int c, int n) {
       uint8_t* y = base + (c & 1) * Cfg::stage + tile_off;
-      uint8_t* y2 = OUT ? y + 2 * Cfg::tile : base + Cfg::mop + (c & 1) * Cfg::tile + tile_off;
+      uint8_t *x = y + 2 * Cfg::tile, *m_place = base + Cfg::mop + tile_off;
+      uint8_t* y2 = OUT ? (exact ? m_place : x) : m_place + (1 + (c & 1)) * Cfg::tile;
+      uint8_t* y3 = OUT ? x : m_place;
       if (i >= n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t at = swz(i, piece + e);
           *reinterpret_cast<uint4*>(y + at) = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(y2 + at) = make_uint4(0, 0, 0, 0);
+          if (exact) *reinterpret_cast<uint4*>(y3 + at) = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(y + Cfg::tile + at) = make_uint4(0, 0, 0, 0);
         }
       } else if (wants_state(c)) {
@@ -459,12 +482,28 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
           const uint4 v = *reinterpret_cast<const uint4*>(y + at);
           const uint32_t in[4] = {v.x, v.y, v.z, v.w};
           uint32_t one[4], two[4];
+          if (exact) {
+            uint32_t three[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 u = lt_mul2(lt_bf2(in[k]), w);
-            one[k] = pack_bf16(u.x, u.y);
-            const float2 rest = lt_fma2(lt_bf2(one[k]), minus, u);
-            two[k] = pack_bf16(rest.x, rest.y);
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = lt_mul2(lt_bf2(in[k]), w);
+              one[k] = pack_bf16(u.x, u.y);
+              float2 rest = lt_fma2(lt_bf2(one[k]), minus, u);
+              // D = 64: both products meet the second terms, so they are halved (exactly)
+              const float2 part = D == 64 ? lt_mul2(rest, make_float2(0.5f, 0.5f)) : rest;
+              two[k] = pack_bf16(part.x, part.y);
+              rest = lt_fma2(lt_bf2(two[k]), D == 64 ? make_float2(-2.0f, -2.0f) : minus, rest);
+              three[k] = pack_bf16(rest.x, rest.y);
+            }
+            *reinterpret_cast<uint4*>(y3 + at) = make_uint4(three[0], three[1], three[2], three[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 u = lt_mul2(lt_bf2(in[k]), w);
+              one[k] = pack_bf16(u.x, u.y);
+              const float2 rest = lt_fma2(lt_bf2(one[k]), minus, u);
+              two[k] = pack_bf16(rest.x, rest.y);
+            }
           }
           *reinterpret_cast<uint4*>(y + at) = make_uint4(one[0], one[1], one[2], one[3]);
           *reinterpret_cast<uint4*>(y2 + at) = make_uint4(two[0], two[1], two[2], two[3]);
@@ -604,6 +643,7 @@ __global__ void __launch_bounds__(LtCfg<D, OUT>::threads, LtCfg<D, OUT>::ctas_pe
       for (int c = 0; c <= chunks; ++c) {
         if (c < chunks) {
           wait(kLtFull + (c & 1), (c >> 1) & 1);
+          if (exact && c > 0) wait(kLtThird, (c - 1) & 1);
           if (!ok) break;
           weight_y(c, min(C, hi - chunk_at(c)));
         }

@@ -1184,6 +1184,7 @@ llsa_status linear_segment_states(const llsa_linear_shape* s, const LinearParams
   A.p[0].init = nullptr;
   A.p[0].transpose = 0;
   A.p[0].out = nullptr;
+  A.p[0].exact = last != nullptr;
   A.p[0].state = states;
   llsa_status st = linear_pass<false>(s, A, cs);
   if (st != LLSA_OK) return st;
@@ -1565,6 +1566,7 @@ llsa_status llsa_linear_forward(const llsa_linear_shape* s, const void* q, const
   } else {
     Q.init = initial_state;
     Q.state = final_state;
+    Q.exact = final_state != nullptr;
   }
   return linear_pass<true>(s, P, cs);
 }
@@ -1604,7 +1606,8 @@ llsa_status llsa_linear_backward(const llsa_linear_shape* s, const void* q, cons
   const bool cut = P.nseg > 1;
   float* back = cut ? static_cast<float*>(workspace) : nullptr;  // the segments' G
   const float f = s->scale;
-  P.p[0] = LinearProblem{sk, sq, sd, dv, cut ? back : d_final, cut ? nullptr : d_initial, f, 1.0f, f, 1, 0};
+  P.p[0] = LinearProblem{sk, sq, sd, dv, cut ? back : d_final, cut ? nullptr : d_initial, f, 1.0f, f, 1, 0,
+                         !cut && d_initial};
   P.p[1] = LinearProblem{sv, sd, sq, dk, cut ? back : d_final, nullptr, f, 1.0f, f, 1, 1};
   P.p[2] = LinearProblem{sd, sv, sk, dq, cut ? states : initial_state, nullptr, f, f, 1.0f, 0, 1};
   if (cut) {

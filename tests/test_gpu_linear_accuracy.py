@@ -76,3 +76,39 @@ def test_bf16_root_mean_square_error(D, N):
         bound = 2.0 ** -16 / 3 ** 0.5 if x.dtype == F32 else (2 / 3) ** 0.5 * 2.0 ** -8
         for h in range(3):
             assert np.linalg.norm(num(x)[:, h] - w[:, h]) <= bound * np.linalg.norm(w[:, h]), (name, h)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,N,cut", [(1, 2, 1, False), (1, 3, 100, False), (1, 2, 1500, True), (100, 2, 290, False),
+                                       (3, 2, 1900, True)])
+def test_returned_states_of_bf16_inputs_are_fp32(D, B, H, N, cut):
+    """The states and their gradients, which are fp32, over ragged rows with NaN behind the last token.  A token
+    enters in three bf16 terms (2^-25 of it) times a weight that is off by a few 2^-24 with either sign, 2^-22 at
+    most; eight products of 16 tokens make a chunk's sum, each cut off below 2^-23 of what the sum is by then,
+    half of that on average and half of the sum over the eight: 2^-22; chunks are added in fp32.  2^-21 together, and
+    a chunk's rounding, 2^-24, that the decay forgets.  (Two terms are 2^-17 off a token, 2.4e-6.)"""
+    shape = llsa.make_linear_shape(B, H, N, D, torch.bfloat16)
+    assert (llsa.llsa_linear_states_elems(shape) > 0) == cut
+    g = torch.Generator(device="cuda").manual_seed(N + D)
+    q, k, v, do = (torch.randn(B, H, N, D, device="cuda", generator=g).bfloat16() for _ in range(4))
+    s0, ds = (torch.randn(B, H, D, D, device="cuda", generator=g) for _ in range(2))
+    lengths = [N - (7 * b) % N for b in range(B)]
+    for t in (q, k, v, do):
+        for b, n in enumerate(lengths):
+            t[b, :, n:] = float("nan")
+    a = torch.tensor([-0.02, -0.7, -0.003][:H], device="cuda")
+    leaves = [t.requires_grad_() for t in (q, k, v, s0)]
+    o, fin = llsa.llsa_linear_attention(q, k, v, a, initial_state=s0, return_state=True,
+                                        lengths=torch.tensor(lengths, device="cuda", dtype=torch.int32))
+    d0 = torch.autograd.grad([o, fin], leaves, [do, ds])[3]
+    rows = sorted({0, 1 % B, B - 1})  # (each row's 64-bit reference takes a while)
+    x = [np.nan_to_num(num(t[rows])) for t in (q, k, v, do)]
+    sub = [lengths[b] for b in rows]
+    _, want, _ = so.linear_forward(*x[:3], num(a), D ** -0.5, num(s0[rows]), sub)
+    dwant = so.linear_backward(*x, num(a), D ** -0.5, num(s0[rows]), sub, num(ds[rows]))[3]
+    for name, got, w in (("final", fin, want), ("d_initial", d0, dwant)):
+        for i in range(len(rows)):
+            for h in range(H):
+                off = np.linalg.norm(num(got[rows[i], h]) - w[i, h])
+                assert off <= 2.0 ** -21 * np.linalg.norm(w[i, h]), (name, i, h, off / np.linalg.norm(w[i, h]))
+    assert llsa.llsa_device_status() == 0
