@@ -205,7 +205,8 @@ def llsa_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log
     ``initial_state``: [B, H, D, D] fp32, the state before the first token (default 0).
     ``lengths``: [B] int32, the tokens of each row of a padded batch; the positions behind them
     take no part and get 0.  ``return_state``: returns (o, state after the last token), which
-    ``llsa_linear_step`` or the next call's ``initial_state`` carries on from.
+    ``llsa_linear_step`` or the next call's ``initial_state`` carries on from (for bf16 the last bits of o may
+    depend on it: a state that is returned keeps more digits of its tokens).
 
     A NaN or infinity at a token may reach the earlier outputs of its chunk of 128 tokens (fp32: 64).
     Before a backward pass is captured into a CUDA graph, drop eager graphs of the same leaves (torch
